@@ -347,6 +347,126 @@ bs_status bs_plan_order(int n_weights, const int* n_blocks, const double* scores
 bs_status bs_plan_budget(long long n_steps, const int* order_weight, int n_weights,
                          const unsigned long long* block_bytes, unsigned long long budget_bytes, int* out_loaded);
 
+/* ------------------------------------------------ packed key/value cache ------ */
+
+/* The other occupant of a serving GPU's variable memory.  Blocks are loaded and
+ * offloaded as the free memory changes (review page, Fig. 2 caption; OpenReview
+ * discussion, reply A1.B); what changes it while a model answers is the keys and
+ * values of the tokens so far.  Here they are held in 4 bits, in pages of a
+ * caller-owned pool, and attention is computed straight from them, as bs_linear
+ * computes from the packed stack.  bs_cache_device_bytes is what a pool takes off the
+ * budget given to bs_plan_budget.
+ *
+ * Numbers.  A token has, per key/value head, D keys and D values, each in groups of 32
+ * consecutive numbers: s = fp16((max - min) / 15), b = fp16(min + 8 (max - min) / 15)
+ * and codes c = rint((x - b) / s + 8) clamped to 0 .. 15 (8 where s is 0), computed in
+ * fp32; the stored number is b + s (c - 8), at most s / 2 plus the two fp16 roundings
+ * (2^-11 |b| + 2^-11 8 s) away from x.  |x| is clamped to 65000, so that every stored
+ * number is finite in fp16, and a NaN is stored as 0: what is stored outlives the call
+ * that stored it, and one NaN would reach the attention of all later tokens.
+ *
+ * Layout.  Page p of the pool is bs_cache_page_bytes bytes at p * bs_cache_page_bytes:
+ * [head][page_tokens / 16] chunks of 20 D bytes.  A chunk holds 16 consecutive tokens:
+ *   [ key codes    16 rows x D / 2 bytes  ][ key (s, b) fp16 pairs    16 x D / 8 bytes ]
+ *   [ value codes  16 rows x D / 2 bytes  ][ value (s, b) fp16 pairs  16 x D / 8 bytes ]
+ * Code word w of a row (32 bits, little endian) holds the codes of dims 8 w .. 8 w + 7,
+ * the first in the lowest four bits.  Keys: row t is token t; word w = 4 g + c stands at
+ * place c D / 32 + g; the pair of group g at place g.  Values: token t is row
+ * t / 2 + 8 (t % 2); word w = r + 8 j (r < 8) stands at place r D / 64 + j; the pair of
+ * group g at place (g % 2) D / 64 + g / 2.  (The attention kernel's lanes then read
+ * whole matrix fragments with single wide loads free of bank conflicts.)  Nothing is
+ * shared between tokens, so a token's bytes are written without reading others.
+ *
+ * Steps.  The calls of one step of a model take the same description of its tokens:
+ * sequence i's new tokens are rows cu_new[i] .. cu_new[i + 1] - 1 of the dense tensors
+ * (row i alone when cu_new is NULL) and stand at positions start[i], start[i] + 1, ...
+ * of the sequence; position t lies in page page_table[i * table_stride + t /
+ * page_tokens].  The three arrays are device memory and are read when the kernels run,
+ * so a captured graph replays with the lengths and pages they hold then.  start[i] < 0
+ * marks an empty slot: nothing is stored for its rows, and they are read and attended
+ * as zeros.  A sequence may hold no new token.  Rows behind the last sequence's are
+ * neither read nor written.  Pages may be shared by sequences that only read them; a
+ * position written twice by one call holds bytes of either row.
+ * The arrays are checked on the device, before anything they point to is touched: a
+ * sequence whose rows leave 0 .. n_tokens - 1, exceed max_new or run backwards, or
+ * whose positions pass its row of the table, is treated as an empty slot, and a page
+ * outside the pool is not written, reads as zeros and is not attended; either sets
+ * the pool's error word (bs_cache_get_device_error: BS_ERR_RANGE).
+ * Head sizes D: 64, 128, 256.  Page sizes: 16, 32, 64, 128 or 256 tokens. */
+typedef struct bs_cache_s* bs_cache_t; /* opaque handle of one layer's pool */
+
+typedef struct {
+  int n_seqs;            /* 1 .. 4096 */
+  int n_tokens;          /* rows of the dense tensors */
+  int max_new;           /* no sequence has more new tokens than this */
+  int table_width;       /* entries of a row of the page table */
+  int table_stride;      /* from one row's first entry to the next one's, >= table_width (any for one row) */
+  const int* cu_new;     /* device, n_seqs + 1 ints, or NULL: one new token a sequence */
+  const int* start;      /* device, n_seqs ints */
+  const int* page_table; /* device, n_seqs x table_stride ints */
+} bs_cache_step;
+
+/* heads * page_tokens * dim * 5 / 4: 4 bits a number and 32 bits a group of 32.  0 for
+ * a shape outside the rules above (heads 1 .. 1024). */
+size_t bs_cache_page_bytes(int heads, int dim, int page_tokens);
+
+/* n_pages * bs_cache_page_bytes rounded up to 256, plus 256 bytes for the pool's device
+ * error word; 0 on invalid arguments. */
+size_t bs_cache_device_bytes(int heads, int dim, int page_tokens, int n_pages);
+
+/* A handle over a caller-owned pool of n_pages pages (>= bs_cache_device_bytes bytes,
+ * 256-aligned) on the current device.  The pages are left as they are; the error word
+ * is cleared on `stream`.  Fails with BS_ERR_NO_DEVICE when the device is not sm_100. */
+bs_status bs_cache_create(int heads, int dim, int page_tokens, int n_pages, void* dev_pages, size_t dev_bytes,
+                          bs_stream_t stream, bs_cache_t* out);
+
+/* Frees the host handle only; device memory stays with the caller. */
+bs_status bs_cache_destroy(bs_cache_t cache);
+
+/* Quantises the step's new keys and values into their pages.  k, v: row r, head h at
+ * k + r * k_token_stride + h * k_head_stride (elements of dtype `dt`, BS_F16, BS_BF16
+ * or BS_F32), dim consecutive numbers; pointers 16-byte aligned, strides multiples of
+ * 16 bytes (0 allowed), so that slices of a joined projection are taken in place.
+ * n_tokens == 0 does nothing.  Asynchronous on `stream`; capturable; the current
+ * device must be the cache's (BS_ERR_INVALID_ARG). */
+bs_status bs_cache_append(bs_cache_t cache, const bs_cache_step* step, const void* k, long long k_token_stride,
+                          long long k_head_stride, const void* v, long long v_token_stride, long long v_head_stride,
+                          bs_dtype dt, bs_stream_t stream);
+
+/* Reads the numbers stored at the step's positions back: k_out, v_out [n_tokens][heads]
+ * [dim] of dtype `dt` (BS_F16, BS_BF16, BS_F32; rounded once from fp32), 16-byte
+ * aligned, either NULL if it is not wanted.  Otherwise as bs_cache_append. */
+bs_status bs_cache_read(bs_cache_t cache, const bs_cache_step* step, void* k_out, void* v_out, bs_dtype dt,
+                        bs_stream_t stream);
+
+/* Workspace of bs_cache_attention for steps of up to step->n_seqs sequences and
+ * step->max_new tokens each (other fields are not read): fp32 partial results of the
+ * contexts that several CTAs share, and their arrival counters.  Zero it once before
+ * its first use; every completed call leaves the counters at zero.  As for bs_linear,
+ * calls that may overlap on the GPU need distinct workspaces.  0 on invalid arguments. */
+size_t bs_cache_attention_workspace_bytes(bs_cache_t cache, const bs_cache_step* step, int q_heads);
+
+/* out[r, h] = sum_t p_t v_t / sum_t p_t, p_t = exp(scale q[r, h] . k_t), over the stored
+ * positions t that row r sees: 0 .. its own, the last `window` of them when window > 0.
+ * Query head h reads key/value head h / (q_heads / heads); q_heads is a multiple of the
+ * cache's heads.  The step's own keys and values are read from the cache, so append
+ * them first (on the same stream).
+ * q as k in bs_cache_append (dtype BS_F16 or BS_BF16); out [n_tokens][q_heads][dim] of
+ * the same dtype, 16-byte aligned; lse (may be NULL) [n_tokens][q_heads] fp32 gets
+ * ln sum_t exp(scale q . k_t), with which results over disjoint contexts are joined.
+ * A row that sees nothing (an empty slot, all its pages outside the pool) gets 0 and
+ * -inf.  Scores, the softmax's maximum and sum and the accumulated output are fp32;
+ * the weights exp(s - max) and the dequantised values enter the product in fp16 (half a
+ * step of fp16 each).  Results do not depend on timing: the same step gives the same
+ * bits.  Asynchronous on `stream`; capturable; the current device must be the cache's. */
+bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const void* q, long long q_token_stride,
+                             long long q_head_stride, int q_heads, bs_dtype dt, float scale, int window, void* out,
+                             float* lse, void* workspace, size_t workspace_bytes, bs_stream_t stream);
+
+/* Synchronises the cache's device, reads and clears the pool's error word: BS_OK,
+ * BS_ERR_RANGE (a step named rows, positions or pages outside their bounds), or BS_ERR_CUDA. */
+bs_status bs_cache_get_device_error(bs_cache_t cache);
+
 /* ------------------------------------------------------------------ errors ----- */
 
 /* Synchronises `stack`'s device, reads and clears the sticky device error word:

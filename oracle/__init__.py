@@ -9,7 +9,8 @@ obviously-correct NumPy implementation in float64 of what the hot path computes:
   (``pack``),
 * weight reconstruction and the linear layer in explicit and factored form
   (``linear``),
-* the global block order and greedy memory-budget fill (``budget``).
+* the global block order and greedy memory-budget fill (``budget``),
+* the packed key/value cache: layout, quantisation, attention (``cache``).
 
 It is test infrastructure: only ``tests/``, ``__graft_entry__.smoke()`` and the
 ``cpu_baseline`` / ``--impl reference`` legs of ``bench.py`` may import it.  It
@@ -31,4 +32,4 @@ Citations name the page and the figure / section they follow:
 Parity status of each function is stated in its docstring; "parity unpinned" marks
 a function no test pins to something other than itself.
 """
-from . import budget, decompose, linear, pack  # noqa: F401
+from . import budget, cache, decompose, linear, pack  # noqa: F401

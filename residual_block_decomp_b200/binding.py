@@ -43,7 +43,15 @@ EXPORTS = (
     "bs_plan_order", "bs_plan_budget", "bs_plain_rank", "bs_plain_block_bytes", "bs_plain_stack_device_bytes",
     "bs_plain_workspace_bytes", "bs_plain_stack_create", "bs_group_workspace_bytes", "bs_linear_group",
     "bs_decompose_workspace_bytes", "bs_decompose",
+    "bs_cache_page_bytes", "bs_cache_device_bytes", "bs_cache_create", "bs_cache_destroy", "bs_cache_append",
+    "bs_cache_read", "bs_cache_attention_workspace_bytes", "bs_cache_attention", "bs_cache_get_device_error",
 )
+
+
+class _Step(ctypes.Structure):   # bs_cache_step
+    _fields_ = [("n_seqs", ctypes.c_int), ("n_tokens", ctypes.c_int), ("max_new", ctypes.c_int),
+                ("table_width", ctypes.c_int), ("table_stride", ctypes.c_int), ("cu_new", ctypes.c_void_p), ("start", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p)]
 
 
 class BsError(RuntimeError):
@@ -85,6 +93,15 @@ def _load():
         "bs_linear_group": (I, [I, P, P, P, P, I, I, P, Z, P]),
         "bs_decompose_workspace_bytes": (Z, [I, I, I]),
         "bs_decompose": (I, [I, I, I, I, P, P, ctypes.c_ulonglong, I, P, Z, P, P, Z, P]),
+        "bs_cache_page_bytes": (Z, [I, I, I]),
+        "bs_cache_device_bytes": (Z, [I, I, I, I]),
+        "bs_cache_create": (I, [I, I, I, I, P, Z, P, ctypes.POINTER(P)]),
+        "bs_cache_destroy": (I, [P]),
+        "bs_cache_append": (I, [P, P, P, LL, LL, P, LL, LL, I, P]),
+        "bs_cache_read": (I, [P, P, P, P, I, P]),
+        "bs_cache_attention_workspace_bytes": (Z, [P, P, I]),
+        "bs_cache_attention": (I, [P, P, P, LL, LL, I, I, ctypes.c_float, I, P, P, P, Z, P]),
+        "bs_cache_get_device_error": (I, [P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -302,3 +319,125 @@ def bs_decompose(W, s, n_blocks: int, records, res_norms_sq, workspace, seed: in
                           records.numel() * records.element_size(), _ptr(res_norms_sq), _ptr(workspace),
                           workspace.numel() * workspace.element_size(), _stream(stream))
     _check(st, "bs_decompose")
+
+
+# ----------------------------------------------------------- packed key/value cache ---
+def bs_cache_page_bytes(heads: int, dim: int, page_tokens: int) -> int:
+    return int(lib.bs_cache_page_bytes(heads, dim, page_tokens))
+
+
+def bs_cache_device_bytes(heads: int, dim: int, page_tokens: int, n_pages: int) -> int:
+    return int(lib.bs_cache_device_bytes(heads, dim, page_tokens, n_pages))
+
+
+def bs_cache_create(heads: int, dim: int, page_tokens: int, n_pages: int, dev_pages, stream=None) -> int:
+    h = ctypes.c_void_p()
+    st = lib.bs_cache_create(heads, dim, page_tokens, n_pages, _ptr(dev_pages),
+                             dev_pages.numel() * dev_pages.element_size(), _stream(stream), ctypes.byref(h))
+    _check(st, "bs_cache_create")
+    _cache_shapes[h.value] = (heads, dim, dev_pages.device)
+    return h.value
+
+
+def bs_cache_destroy(handle: int) -> None:
+    _check(lib.bs_cache_destroy(handle), "bs_cache_destroy")
+    _cache_shapes.pop(handle, None)
+
+
+_cache_shapes: dict[int, tuple] = {}   # (heads, dim, device) of live handles, for the tensors' checks
+
+
+def _ints(t, name: str, shape: tuple) -> int:
+    import torch
+    if t.dtype != torch.int32 or t.dim() != len(shape) or any(s is not None and n != s for n, s in zip(t.shape, shape)):
+        raise ValueError(f"{name}: need an int32 tensor of shape {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+class CacheStep:
+    """A step's tokens for the cache calls (bs_cache_step): ``start`` (n_seqs int32, on
+    the GPU), ``page_table`` (n_seqs x entries int32), ``n_tokens`` rows in the dense
+    tensors, at most ``max_new`` of a sequence, ``cu_new`` (n_seqs + 1 int32) or None for
+    one new token a sequence.  Keeps the tensors alive; their contents are read when the
+    kernels run and may change between calls."""
+
+    def __init__(self, start, page_table, n_tokens: int, max_new: int = 1, cu_new=None):
+        self.start, self.page_table, self.cu_new = start, page_table, cu_new
+        self.n_tokens, self.max_new = int(n_tokens), int(max_new)
+        ps = _ints(start, "start", (None,))
+        n = start.shape[0]
+        pt = _ints(page_table, "page_table", (n, None))
+        pc = None if cu_new is None else _ints(cu_new, "cu_new", (n + 1,))
+        self.device = start.device
+        if page_table.device != start.device or (cu_new is not None and cu_new.device != start.device):
+            raise ValueError("start, page_table and cu_new must be on one device")
+        self.c = _Step(n, self.n_tokens, self.max_new, page_table.shape[1], page_table.stride(0), pc, ps, pt)
+        self.ref = ctypes.byref(self.c)
+
+
+def _rows(t, name: str, handle: int, step: CacheStep, query: bool = False) -> tuple:
+    """(pointer, token stride, head stride) of a tensor [n_tokens, heads, dim] with contiguous numbers
+    on the cache's GPU; a query's heads are a multiple of the cache's (checked by the library)."""
+    heads, dim, device = _cache_shapes.get(handle, (None, None, None))
+    if t.dim() != 3 or t.shape[0] != step.n_tokens or t.shape[2] != dim or not (query or t.shape[1] == heads):
+        raise ValueError(f"{name}: need [{step.n_tokens}, {'q_heads' if query else heads}, {dim}], got {list(t.shape)}")
+    tok, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name}: the numbers of a head must be contiguous")
+    if t.device != device or step.device != device:
+        raise ValueError(f"{name}: tensors and step must be on the cache's device {device}")
+    return t.data_ptr(), tok, head
+
+
+def bs_cache_append(handle: int, step: CacheStep, k, v, stream=None) -> None:
+    """Quantises k and v [n_tokens, heads, dim] (any token and head strides) into the
+    pages of the step's positions."""
+    if k.dtype != v.dtype:
+        raise ValueError("k and v must have one dtype")
+    st = lib.bs_cache_append(handle, step.ref, *_rows(k, "k", handle, step), *_rows(v, "v", handle, step),
+                             _dtype_code(k), _stream(stream))
+    _check(st, "bs_cache_append")
+
+
+def bs_cache_read(handle: int, step: CacheStep, k_out, v_out, stream=None) -> None:
+    """Writes the numbers stored at the step's positions to k_out and v_out (contiguous
+    [n_tokens, heads, dim]; either may be None)."""
+    outs = [t for t in (k_out, v_out) if t is not None]
+    for t in outs:
+        _rows(t, "k_out, v_out", handle, step)
+        if not t.is_contiguous() or t.dtype != outs[0].dtype:
+            raise ValueError("k_out and v_out must be contiguous and of one dtype")
+    st = lib.bs_cache_read(handle, step.ref, _ptr(k_out), _ptr(v_out), _dtype_code(outs[0]) if outs else 0,
+                           _stream(stream))
+    _check(st, "bs_cache_read")
+
+
+def bs_cache_attention_workspace_bytes(handle: int, step: CacheStep, q_heads: int) -> int:
+    return int(lib.bs_cache_attention_workspace_bytes(handle, step.ref, q_heads))
+
+
+def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: float | None = None, window: int = 0,
+                       lse=None, stream=None) -> None:
+    """out = attention of q [n_tokens, q_heads, dim] over the stored positions each row
+    sees; ``scale`` defaults to dim ** -0.5, ``window`` 0 is unlimited, ``lse``
+    [n_tokens, q_heads] fp32 or None."""
+    import torch
+    ptr, tok, head = _rows(q, "q", handle, step, True)
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+        raise ValueError("out must be contiguous, with q's shape, dtype and device")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or
+                            lse.device != q.device):
+        raise ValueError("lse must be contiguous fp32 [n_tokens, q_heads] on q's device")
+    if workspace is not None and workspace.device != q.device:
+        raise ValueError("the workspace must be on q's device")
+    st = lib.bs_cache_attention(handle, step.ref, ptr, tok, head, q.shape[1], _dtype_code(q),
+                                q.shape[2] ** -0.5 if scale is None else scale, window, out.data_ptr(), _ptr(lse),
+                                _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                _stream(stream))
+    _check(st, "bs_cache_attention")
+
+
+def bs_cache_get_device_error(handle: int) -> int:
+    return int(lib.bs_cache_get_device_error(handle))

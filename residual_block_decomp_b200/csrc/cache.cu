@@ -1,0 +1,282 @@
+// The packed key/value cache: quantising new tokens into their pages, and reading them
+// back.  The layout of a page and the arithmetic of a group are stated in
+// include/bitstack.h.
+//
+// Both kernels work in units of one code word, 8 consecutive numbers of one (token,
+// head, keys or values): a thread moves 16 bytes of dense numbers (32 for fp32), four
+// neighbouring lanes hold a group of 32, and a warp covers whole rows, so dense accesses
+// are contiguous and packed ones stay within a row's 32 to 128 bytes.
+//
+// A group is s = fp16((max - min) / 15), b = fp16(min + 8 (max - min) / 15),
+// c = rint((x - b) / s + 8).  The quotient is a true division and the statistics are
+// taken in fp32, so the codes are those of the definition for every input.
+//
+// Both are bound by memory traffic: 4 bytes dense and 1.25 packed a number pair.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cache.h"
+
+namespace bs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr float kCacheClamp = 65000.0f;   // b + s (c - 8) then stays below fp16's 65504 with both roundings
+
+// Where word w and pair g of a row stand, and token t's row (keys in order, values as
+// the attention kernel's fragments want them).
+template <int D>
+__device__ __forceinline__ int word_place(bool value, int w) {
+  return value ? (w & 7) * (D / 64) + (w >> 3) : (w & 3) * (D / 32) + (w >> 2);
+}
+template <int D>
+__device__ __forceinline__ int pair_place(bool value, int g) {
+  return value ? (g & 1) * (D / 64) + (g >> 1) : g;
+}
+__device__ __forceinline__ int token_row(bool value, int t) { return value ? (t >> 1) + 8 * (t & 1) : t; }
+
+// One unit of a sequence: word w of token i, head h, keys (value false) or values.
+template <int D>
+struct Unit {
+  int w, h, i;
+  bool value;
+  __device__ Unit(unsigned u, int heads) {
+    w = u % (D / 8);
+    u /= D / 8;
+    value = u & 1;
+    u >>= 1;
+    i = static_cast<int>(u / static_cast<unsigned>(heads));
+    h = static_cast<int>(u % static_cast<unsigned>(heads));
+  }
+};
+
+// Address of a unit's code word; its pair is at the returned `pair`.
+template <int D>
+__device__ __forceinline__ uint32_t* unit_bytes(const StepParams& p, int seq, int start, const Unit<D>& u,
+                                                uint32_t** pair) {
+  const int pos = start + u.i;
+  const int page = p.table[static_cast<size_t>(seq) * p.stride + (pos >> p.page_shift)];
+  uint8_t* c = chunk_at(p, page, pos, u.h, D);
+  if (c == nullptr) return nullptr;
+  if (u.value) c += 10 * D;
+  const int row = token_row(u.value, pos & (kChunkTokens - 1));
+  *pair = reinterpret_cast<uint32_t*>(c + 8 * D + row * (D / 8)) + pair_place<D>(u.value, u.w >> 2);
+  return reinterpret_cast<uint32_t*>(c + row * (D / 2)) + word_place<D>(u.value, u.w);
+}
+
+template <typename T>
+struct Eight;   // 8 dense numbers
+template <>
+struct Eight<__half> {
+  uint4 a;
+  __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r[e]));
+      x[2 * e] = f.x;
+      x[2 * e + 1] = f.y;
+    }
+  }
+  __device__ static void store(void* p, const float (&x)[8]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __half2 h = __floats2half2_rn(x[2 * e], x[2 * e + 1]);
+      r[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *static_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 a;
+  __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void get(float (&x)[8]) const {
+    const uint32_t r[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(r[e] << 16);
+      x[2 * e + 1] = __uint_as_float(r[e] & 0xffff0000u);
+    }
+  }
+  __device__ static void store(void* p, const float (&x)[8]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+      r[e] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *static_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+  }
+};
+template <>
+struct Eight<float> {
+  float4 a, b;
+  __device__ void load(const void* p) {
+    a = __ldg(static_cast<const float4*>(p));
+    b = __ldg(static_cast<const float4*>(p) + 1);
+  }
+  __device__ void get(float (&x)[8]) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+  __device__ static void store(void* p, const float (&x)[8]) {
+    static_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    static_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+  }
+};
+
+// grid: (blocks of units of a sequence, sequences); U units a thread, all loads first.
+template <int D, typename T, int U>
+__global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ CacheCopyParams p) {
+  const int seq = blockIdx.y;
+  const SeqSpan s = seq_span(p.st, seq);
+  if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
+  if (!s.live) return;
+  const unsigned units = static_cast<unsigned>(s.rows) * p.st.heads * 2 * (D / 8);
+  for (unsigned base = blockIdx.x * (kThreads * U); base < units; base += gridDim.x * (kThreads * U)) {
+    Eight<T> in[U];
+    uint32_t *word[U], *pair[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const unsigned u = base + e * kThreads + threadIdx.x;
+      word[e] = nullptr;
+      in[e] = Eight<T>{};
+      if (u < units) {
+        const Unit<D> un(u, p.st.heads);
+        const int kv = un.value ? 1 : 0;
+        in[e].load(static_cast<const T*>(p.in[kv]) + (s.row0 + un.i) * p.tok[kv] + un.h * p.head[kv] + un.w * 8);
+        word[e] = unit_bytes<D>(p.st, seq, s.start, un, &pair[e]);
+        if (word[e] == nullptr) atomicOr(p.st.err, kErrRange);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      float x[8];
+      in[e].get(x);
+      float lo = kCacheClamp, hi = -kCacheClamp;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        x[k] = x[k] != x[k] ? 0.0f : fminf(fmaxf(x[k], -kCacheClamp), kCacheClamp);
+        lo = fminf(lo, x[k]);
+        hi = fmaxf(hi, x[k]);
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      }
+      const float step = __fdiv_rn(hi - lo, 15.0f);
+      const __half sh = __float2half_rn(step), bh = __float2half_rn(fmaf(8.0f, step, lo));
+      const float sf = __half2float(sh), bf = __half2float(bh);
+      uint32_t w = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float c = sf > 0.0f ? rintf(__fadd_rn(__fdiv_rn(x[k] - bf, sf), 8.0f)) : 8.0f;
+        w |= static_cast<uint32_t>(fminf(fmaxf(c, 0.0f), 15.0f)) << (4 * k);
+      }
+      if (word[e] != nullptr) {
+        *word[e] = w;
+        if ((threadIdx.x & 3) == 0)
+          *pair[e] = static_cast<uint32_t>(__half_as_ushort(sh)) | static_cast<uint32_t>(__half_as_ushort(bh)) << 16;
+      }
+    }
+  }
+}
+
+// grid as above.  Rows of an empty slot, and of pages outside the pool, are zeros.
+template <int D, typename T, int U>
+__global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheCopyParams p) {
+  const int seq = blockIdx.y;
+  const SeqSpan s = seq_span(p.st, seq);
+  if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
+  const unsigned units = static_cast<unsigned>(s.rows) * p.st.heads * 2 * (D / 8);
+  for (unsigned base = blockIdx.x * (kThreads * U); base < units; base += gridDim.x * (kThreads * U)) {
+    uint32_t word[U], pair[U];
+    T* to[U];
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      const unsigned u = base + e * kThreads + threadIdx.x;
+      word[e] = pair[e] = 0;
+      to[e] = nullptr;
+      if (u < units) {
+        const Unit<D> un(u, p.st.heads);
+        T* out = static_cast<T*>(p.out[un.value ? 1 : 0]);
+        if (out == nullptr) continue;
+        to[e] = out + (static_cast<size_t>(s.row0 + un.i) * p.st.heads + un.h) * D + un.w * 8;
+        if (!s.live) continue;
+        uint32_t* pp;
+        const uint32_t* wp = unit_bytes<D>(p.st, seq, s.start, un, &pp);
+        if (wp == nullptr) {
+          atomicOr(p.st.err, kErrRange);
+        } else {
+          word[e] = *wp;
+          pair[e] = *pp;
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < U; ++e) {
+      if (to[e] == nullptr) continue;
+      const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pair[e]));
+      float x[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[k] = fmaf(sb.x, static_cast<float>((word[e] >> (4 * k)) & 15u) - 8.0f, sb.y);
+      Eight<T>::store(to[e], x);
+    }
+  }
+}
+
+// Blocks for the longest sequence the step may hold; sequences loop over theirs.
+template <int D, int U>
+dim3 copy_grid(const StepParams& s) {
+  const long long longest = s.max_new < s.n_tokens ? s.max_new : s.n_tokens;
+  const long long units = longest * s.heads * 2 * (D / 8);
+  const long long blocks = (units + kThreads * U - 1) / (kThreads * U);
+  return dim3(static_cast<unsigned>(blocks < 1 ? 1 : (blocks > 65535 ? 65535 : blocks)), static_cast<unsigned>(s.n_seqs));
+}
+
+template <int D, typename T>
+cudaError_t append_as(const CacheCopyParams& p, cudaStream_t stream) {
+  const long long units = static_cast<long long>(p.st.n_tokens) * p.st.heads * 2 * (D / 8);
+  if (units >= 148ll * 8 * kThreads * 4)
+    cache_append_kernel<D, T, 4><<<copy_grid<D, 4>(p.st), kThreads, 0, stream>>>(p);
+  else
+    cache_append_kernel<D, T, 1><<<copy_grid<D, 1>(p.st), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t read_as(const CacheCopyParams& p, cudaStream_t stream) {
+  const long long units = static_cast<long long>(p.st.n_tokens) * p.st.heads * 2 * (D / 8);
+  if (units >= 148ll * 8 * kThreads * 4)
+    cache_read_kernel<D, T, 4><<<copy_grid<D, 4>(p.st), kThreads, 0, stream>>>(p);
+  else
+    cache_read_kernel<D, T, 1><<<copy_grid<D, 1>(p.st), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+template <int D>
+cudaError_t append_dim(const CacheCopyParams& p, int dtype, cudaStream_t stream) {
+  return dtype == BS_F16 ? append_as<D, __half>(p, stream)
+         : dtype == BS_BF16 ? append_as<D, __nv_bfloat16>(p, stream) : append_as<D, float>(p, stream);
+}
+template <int D>
+cudaError_t read_dim(const CacheCopyParams& p, int dtype, cudaStream_t stream) {
+  return dtype == BS_F16 ? read_as<D, __half>(p, stream)
+         : dtype == BS_BF16 ? read_as<D, __nv_bfloat16>(p, stream) : read_as<D, float>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream) {
+  return dim == 64 ? append_dim<64>(p, dtype, stream)
+         : dim == 128 ? append_dim<128>(p, dtype, stream) : append_dim<256>(p, dtype, stream);
+}
+cudaError_t launch_cache_read(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream) {
+  return dim == 64 ? read_dim<64>(p, dtype, stream)
+         : dim == 128 ? read_dim<128>(p, dtype, stream) : read_dim<256>(p, dtype, stream);
+}
+
+}  // namespace bs

@@ -1,0 +1,110 @@
+// Internal declarations of the packed key/value cache: the handle, the layout of a
+// chunk, and the step's description as the kernels take it.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/bitstack.h"
+
+namespace bs {
+
+constexpr int kChunkTokens = 16;     // tokens of a chunk: one matrix tile's rows
+constexpr int kCacheMaxSeqs = 4096;  // sequences of a step (their tile counts are prefix-summed in shared memory)
+constexpr uint32_t kErrRange = 2u;   // device error word bit: a step left its bounds
+
+__host__ __device__ constexpr int chunk_bytes(int dim) { return 20 * dim; }
+
+// A step as the kernels take it (pointers to device memory).
+struct StepParams {
+  uint8_t* pages;
+  unsigned long long page_bytes;
+  uint32_t* err;
+  const int* cu;
+  const int* start;
+  const int* table;
+  int n_seqs, n_tokens, max_new, width, stride;   // width, stride: entries of a table row, and between rows
+  int n_pages, heads;
+  int page_shift;                    // log2 of the tokens of a page
+};
+
+// What a step says of one sequence, after its checks: `rows` new tokens from row `row0`
+// at positions start ..; `live` false where nothing is stored or attended.
+struct SeqSpan {
+  int row0, rows, start;
+  bool live, bad;
+};
+__device__ __forceinline__ SeqSpan seq_span(const StepParams& p, int i) {
+  SeqSpan s;
+  long long lo, hi;
+  if (p.cu != nullptr) {
+    lo = p.cu[i];
+    hi = p.cu[i + 1];
+  } else {
+    lo = i;
+    hi = i + 1;
+  }
+  const int start = p.start[i];
+  s.bad = lo < 0 || hi < lo || hi > p.n_tokens;
+  s.row0 = static_cast<int>(lo);
+  s.rows = s.bad ? 0 : static_cast<int>(hi - lo);
+  s.start = start;
+  s.live = !s.bad && start >= 0 && s.rows > 0;
+  if (s.live && (s.rows > p.max_new ||
+                 static_cast<long long>(start) + s.rows > (static_cast<long long>(p.width) << p.page_shift))) {
+    s.live = false;
+    s.bad = true;
+  }
+  return s;
+}
+
+// Device bytes of the chunk that holds `pos` of sequence i, head h; nullptr for a page
+// outside the pool.
+__device__ __forceinline__ uint8_t* chunk_at(const StepParams& p, int page, int pos, int h, int dim) {
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(p.n_pages)) return nullptr;
+  const int cpp = (1 << p.page_shift) / kChunkTokens;
+  const int c = (pos & ((1 << p.page_shift) - 1)) / kChunkTokens;
+  return p.pages + static_cast<unsigned long long>(page) * p.page_bytes +
+         static_cast<unsigned long long>(h * cpp + c) * chunk_bytes(dim);
+}
+
+// Attention over the cache: arguments and workspace carve-up.
+struct CacheAttnParams {
+  StepParams st;
+  const void* q;
+  long long q_tok, q_head;           // strides in elements
+  int q_heads, group;
+  int bf16, window;
+  float scale_log2;                  // scale * log2(e): scores are kept in the log2 domain
+  void* out;
+  float* lse;
+  uint32_t* cnt;                     // [grid] arrivals of the item that begins in CTA i's range and leaves it
+  float* part;                       // [grid][2] partial results
+  int grid;
+};
+struct CacheAttnWs {
+  size_t cnt, part, total;
+};
+CacheAttnWs cache_attn_ws(int dim, int rows, int sms);
+cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream);
+
+struct CacheCopyParams {
+  StepParams st;
+  const void* in[2];                 // keys, values (append)
+  void* out[2];                      // keys, values (read)
+  long long tok[2], head[2];         // strides of `in` in elements
+};
+cudaError_t launch_cache_append(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);
+cudaError_t launch_cache_read(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);
+
+}  // namespace bs
+
+// The handle.  Host memory only.
+struct bs_cache_s {
+  int heads, dim, page_tokens, n_pages;
+  uint8_t* pages;
+  size_t page_bytes;
+  uint32_t* err;
+  int device, sm_count;
+};

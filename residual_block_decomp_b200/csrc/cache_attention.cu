@@ -1,0 +1,817 @@
+// Attention over the packed key/value cache, for few query rows per key/value head (the
+// tokens a model generates; include/bitstack.h, bs_cache_attention).
+//
+//     o_r = sum_t p_rt v_t / sum_t p_rt,   p_rt = 2^(x_rt - m_r),   x_rt = scale log2(e) q_r . k_t
+//
+// in one pass over the packed pages with a running maximum m and sum: every packed byte
+// is read once, 1.25 D bytes a (token, head), and nothing dense is written.
+//
+// Work.  An item is one (sequence, head, tile of R = 8 NT query rows); its context is cut
+// into tiles of 5120 packed bytes (64, 32 or 16 tokens for D = 64, 128, 256).  The tiles of all
+// items form one list, split evenly over the CTAs and, inside a CTA, over its warps, so that one long
+// context and many short ones keep all SMs equally busy whatever the lengths (which only the device
+// knows).  A warp streams its run of tiles through its own ring of shared-memory stages with
+// 16-byte asynchronous copies and never waits for another warp.  What is left of items that several
+// warps share is joined in shared memory, of items that several CTAs share in the workspace by the CTA
+// that arrives last; both add in the order of the tiles, so results do not depend on timing.
+//
+// Products.  Tokens are the M side of mma.m16n8k16 and query rows its N side (8 rows: the
+// heads that share a key/value head), so few rows waste little.  tcgen05 would need 128
+// rows of queries or would take the keys through shared memory as dense operands; here
+// the codes go from their packed words to fragments in registers.
+//  * Keys: a lane's words give the fragments of its tokens directly: (word >> s) & 0x00f000f0
+//    | 0x5400 is the pair 64 + c in fp16, exact.  Per group of 32: acc = sum (64 + c) q, and with
+//    the token's pair (s, b): s acc + (b - 72 s) sum q = sum (b + s (c - 8)) q, in fp32.  No per-number
+//    arithmetic is needed, and a code's product with q is exact.
+//  * Softmax: the accumulator layout holds rows = tokens, columns = query rows; the maximum over tokens
+//    is three shuffles, and movmatrix turns the fp16 weights into the next product's
+//    B fragment.
+//  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
+//    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).
+//    Scales cannot stay outside the product here as for keys: the token is what is summed over.
+//
+// Queries are taken as fp16.  fp16 inputs are exact; a bf16 row is first scaled by a power of two that
+// brings its largest entry into [1, 2) (undone in the fp32 scores): exact down to
+// 2^-14 of that entry, and within 2^-25 of it below.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cache.h"
+#include "ptx.cuh"
+
+namespace bs {
+namespace {
+
+constexpr int kTileBytes5k = 5120;
+constexpr float kNegInf = -INFINITY;
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int TILE = 4096 / D;                       // tokens of a tile: 5120 packed bytes
+  static constexpr int TM = TILE / kChunkTokens;              // chunks of a tile
+  static constexpr int GR = D / 32;                           // groups of a row
+  static constexpr int J = D / 64;                            // value words of a lane and token
+  static constexpr int R = 8 * NT;                            // query rows of an item
+  static constexpr int OREG = NT * J * 16;                    // accumulators of a lane
+  static constexpr int FREG = OREG + 4 * NT;                  // and its maxima and sums
+  static constexpr int FBYTES = FREG * 128;                   // a warp's partial result
+  static constexpr int NW = (NT == 1 && D <= 128) ? 12 : 8;   // warps
+  static constexpr int ST = 2;                                // stages of a warp
+};
+
+// Partial results are laid out [register][lane].
+struct FragMeta {
+  long long id;          // number of the item's first tile in the list; -1: no partial result here
+  int tiles, seq, h, rt;
+};
+
+__device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
+  uint32_t d;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool fill) {
+  const int n = fill ? 16 : 0;
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+// (word & 0x00f000f0) | 0x54005400: nibbles 1 and 5 of a word as the fp16 pair 64 + c.
+__device__ __forceinline__ uint32_t pair64(uint32_t w) { return (w & 0x00f000f0u) | 0x54005400u; }
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+template <int N>
+__device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
+  if constexpr (N == 1) {
+    r[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    r[0] = v.x; r[1] = v.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+    }
+  }
+}
+
+// A place in the list of tiles: item (seq, h, rt) and tile t of its `tiles`.
+struct Cursor {
+  int seq, h, rt, t, tiles, rts, first;   // first: the position the item's tiles begin at (a multiple of 16)
+  int row0, rows, start, end;             // the sequence's rows and positions; end: positions seen
+};
+
+template <int D, int NT>
+struct Shared {
+  using C = Cfg<D, NT>;
+  uint8_t stage[C::NW][C::ST][kTileBytes5k];
+  uint8_t frag[C::NW][C::FBYTES];         // a warp's partial result of its first item; of its last one: in its stages
+  FragMeta meta[2 * C::NW];
+  int scan[32];
+  int last[2];
+  long long scan_total;
+  // then long long prefix[n_seqs + 1]
+};
+
+template <int D, int NT>
+struct Worker {
+  using C = Cfg<D, NT>;
+  const CacheAttnParams& p;
+  const long long* prefix;
+  int lane;
+
+  // Rows, positions and tile count of sequence i (tiles 0 where nothing is attended).
+  __device__ void seq(Cursor& c, int i) const {
+    const SeqSpan s = seq_span(p.st, i);
+    c.seq = i;
+    c.row0 = s.row0;
+    c.rows = s.rows;
+    c.start = s.start;
+    c.end = s.start + s.rows;
+    c.first = 0;
+    c.tiles = 0;
+    c.rts = 0;
+    if (!s.live) return;
+    if (p.window > 0 && s.start >= p.window) c.first = (s.start - p.window + 1) / kChunkTokens * kChunkTokens;
+    c.tiles = (c.end - c.first + C::TILE - 1) / C::TILE;
+    c.rts = (s.rows * p.group + C::R - 1) / C::R;
+  }
+  __device__ void seek(Cursor& c, long long tile) const {
+    int lo = 0, hi = p.st.n_seqs - 1;      // the last sequence whose tiles begin at or before `tile`
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (prefix[mid] <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    seq(c, lo);
+    const unsigned off = static_cast<unsigned>(tile - prefix[lo]);
+    const unsigned item = off / c.tiles;
+    c.t = off % c.tiles;
+    c.h = item / c.rts;
+    c.rt = item % c.rts;
+  }
+  __device__ void next_item(Cursor& c) const {
+    c.t = 0;
+    if (++c.rt < c.rts) return;
+    c.rt = 0;
+    if (++c.h < p.st.heads) return;
+    c.h = 0;
+    int i = c.seq + 1;
+    while (i < p.st.n_seqs - 1 && prefix[i + 1] == prefix[i]) ++i;
+    if (i < p.st.n_seqs) seq(c, i);
+  }
+
+  // Requests tile c.t of the item into `stage`; returns which of its chunks are in the pool.
+  __device__ uint32_t request(const Cursor& c, uint32_t stage) const {
+    const uint8_t* src[C::TM];
+    uint32_t ok = 0;
+#pragma unroll
+    for (int m = 0; m < C::TM; ++m) {
+      const int pos = c.first + c.t * C::TILE + m * kChunkTokens;
+      src[m] = nullptr;
+      if (pos < c.end) {
+        const int page = __ldg(p.st.table + static_cast<size_t>(c.seq) * p.st.stride + (pos >> p.st.page_shift));
+        src[m] = chunk_at(p.st, page, pos, c.h, D);
+        if (src[m] != nullptr) ok |= 1u << m;
+        else if (lane == 0) atomicOr(p.st.err, kErrRange);
+      }
+    }
+    constexpr int UC = chunk_bytes(D) / 16;   // 16-byte units of a chunk
+#pragma unroll
+    for (int k = 0; k < kTileBytes5k / 512; ++k) {
+      const int u = k * 32 + lane;
+      int m, o;                               // chunk, and unit inside it
+      if constexpr (D == 64) {
+        const int half = k / 5;               // 160 units: two chunks
+        const int v = u - half * 160;
+        m = 2 * half + (v >= UC ? 1 : 0);
+        o = v >= UC ? v - UC : v;
+      } else {
+        m = k / (UC / 32);
+        o = u - m * UC;
+      }
+      const uint8_t* base = src[0];
+#pragma unroll
+      for (int i = 1; i < C::TM; ++i)
+        if (m == i) base = src[i];
+      int d = o;
+      if constexpr (D == 256) {               // rows of 128 bytes: spread the lanes' units over the banks
+        if (o < 128) d = o ^ ((o >> 3) & 1);
+        else if (o >= 160 && o < 288) d = o ^ ((((o - 160) >> 3) & 3) << 1);
+      }
+      cp16_zfill(stage + (m * UC + d) * 16, base == nullptr ? p.st.pages : base + o * 16, base != nullptr);
+    }
+    return ok;
+  }
+};
+
+// The rows of an item as a lane needs them: query fragments (its row's numbers), and for
+// the accumulator columns 2 (lane % 4) + {0, 1}: sums over groups, score factors, positions.
+template <int D, int NT>
+struct Rows {
+  using C = Cfg<D, NT>;
+  uint32_t q[NT][C::GR][4];
+  float sum[NT][C::GR][2];
+  float factor[NT][2];
+  int pos[NT][2];        // position of the row's token; -1: no such row
+  int lowest, highest;   // positions of the item's first and last row
+
+  __device__ void load(const CacheAttnParams& p, const Cursor& c, int lane) {
+    const int n = lane >> 2, cc = lane & 3;
+    const int total = c.rows * p.group;
+    lowest = c.start + c.rt * C::R / p.group;
+    highest = c.start + (min((c.rt + 1) * C::R, total) - 1) / p.group;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = c.rt * C::R + nt * 8 + n;
+      const int i = row / p.group, g = row % p.group;
+      const uint16_t* src = static_cast<const uint16_t*>(p.q) + (c.row0 + i) * p.q_tok +
+                            static_cast<long long>(c.h * p.group + g) * p.q_head + cc * 8;
+      uint4 raw[C::GR];
+#pragma unroll
+      for (int gr = 0; gr < C::GR; ++gr)
+        raw[gr] = row < total ? __ldg(reinterpret_cast<const uint4*>(src + gr * 32)) : make_uint4(0, 0, 0, 0);
+      float back = 1.0f;
+      if (p.bf16) {
+        uint32_t top = 0;   // exponent bits of the row's largest entry
+#pragma unroll
+        for (int gr = 0; gr < C::GR; ++gr) {
+          const uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = max(top, max(r[e] & 0x7f800000u, (r[e] << 16) & 0x7f800000u));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^-e for a finite normal exponent e below 127; inf and NaN rows, and rows of zeros and
+        // subnormals, are taken unscaled or by the smallest normal
+        uint32_t up = 254u << 23;
+        float scale = 1.0f;
+        if (top != 0x7f800000u) {
+          if (top == 0) top = 1u << 23;
+          back = __uint_as_float(top);
+          scale = __uint_as_float(up - top);
+          if (top == up) scale = 0x1p-127f;   // e = 127: 2^-127, a subnormal factor, exact
+        }
+#pragma unroll
+        for (int gr = 0; gr < C::GR; ++gr) {
+          uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(r[e] << 16) * scale, hi = __uint_as_float(r[e] & 0xffff0000u) * scale;
+            r[e] = h2u(__floats2half2_rn(lo, hi));
+          }
+          raw[gr] = make_uint4(r[0], r[1], r[2], r[3]);
+        }
+      }
+      const float f = p.scale_log2 * back;
+#pragma unroll
+      for (int gr = 0; gr < C::GR; ++gr) {
+        // numbers (d, d + 4) pair up as the codes of a word do
+        q[nt][gr][0] = __byte_perm(raw[gr].x, raw[gr].z, 0x5410);
+        q[nt][gr][1] = __byte_perm(raw[gr].x, raw[gr].z, 0x7632);
+        q[nt][gr][2] = __byte_perm(raw[gr].y, raw[gr].w, 0x5410);
+        q[nt][gr][3] = __byte_perm(raw[gr].y, raw[gr].w, 0x7632);
+        float s = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = __half22float2(u2h(q[nt][gr][e]));
+          s += v.x + v.y;
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        sum[nt][gr][0] = __shfl_sync(0xffffffffu, s, 8 * cc);
+        sum[nt][gr][1] = __shfl_sync(0xffffffffu, s, 8 * cc + 4);
+      }
+      const int at = row < total ? c.start + i : -1;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        factor[nt][k] = __shfl_sync(0xffffffffu, f, 8 * cc + 4 * k);
+        pos[nt][k] = __shfl_sync(0xffffffffu, at, 8 * cc + 4 * k);
+      }
+    }
+  }
+};
+
+// Running softmax state and output of a warp for its item.
+template <int D, int NT>
+struct State {
+  using C = Cfg<D, NT>;
+  float o[NT][C::J][4][4];
+  float m[NT][2], l[NT][2];   // l: this lane's tokens only until reduce()
+
+  __device__ void clear() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < C::J; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] = 0.0f;
+      m[nt][0] = m[nt][1] = kNegInf;
+      l[nt][0] = l[nt][1] = 0.0f;
+    }
+  }
+  __device__ void reduce() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 *= 2) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o2);
+  }
+
+  // One tile: positions pos0 .., of which `ok` chunks hold tokens; `masked`: some (row, token) is hidden.
+  __device__ void tile(const Rows<D, NT>& q, const uint8_t* st, int pos0, int end, uint32_t ok, bool masked, int window,
+                       int lane) {
+    const int t = lane >> 2, cc = lane & 3;
+    float s[C::TM][NT][4];
+#pragma unroll
+    for (int mt = 0; mt < C::TM; ++mt) {
+      const uint8_t* ch = st + mt * chunk_bytes(D);
+      uint32_t wa[C::GR], wb[C::GR], pa[C::GR], pb[C::GR];
+      if constexpr (D == 256) {
+        const int x = t & 1;   // units are swapped in odd rows
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t r[4];
+          lds<4>(r, ch + t * 128 + ((cc * 2 + i) ^ x) * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) wa[4 * i + e] = r[e];
+          lds<4>(r, ch + (t + 8) * 128 + ((cc * 2 + i) ^ x) * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) wb[4 * i + e] = r[e];
+        }
+      } else {
+        lds<C::GR>(wa, ch + t * (D / 2) + cc * (D / 8));
+        lds<C::GR>(wb, ch + (t + 8) * (D / 2) + cc * (D / 8));
+      }
+      lds<C::GR>(pa, ch + 8 * D + t * (D / 8));
+      lds<C::GR>(pb, ch + 8 * D + (t + 8) * (D / 8));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
+#pragma unroll
+      for (int g = 0; g < C::GR; ++g) {
+        const float2 fa = __half22float2(u2h(pa[g])), fb = __half22float2(u2h(pb[g]));
+        const float ta = fmaf(-72.0f, fa.x, fa.y), tb = fmaf(-72.0f, fb.x, fb.y);
+        const uint32_t a0 = pair64(wa[g] << 4), a1 = pair64(wb[g] << 4);
+        const uint32_t a2 = pair64(wa[g]), a3 = pair64(wb[g]);
+        const uint32_t a4 = pair64(wa[g] >> 4), a5 = pair64(wb[g] >> 4);
+        const uint32_t a6 = pair64(wa[g] >> 8), a7 = pair64(wb[g] >> 8);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          mma16816(acc, a0, a1, a2, a3, q.q[nt][g][0], q.q[nt][g][1]);
+          mma16816(acc, a4, a5, a6, a7, q.q[nt][g][2], q.q[nt][g][3]);
+          s[mt][nt][0] = fmaf(fa.x, acc[0], fmaf(ta, q.sum[nt][g][0], s[mt][nt][0]));
+          s[mt][nt][1] = fmaf(fa.x, acc[1], fmaf(ta, q.sum[nt][g][1], s[mt][nt][1]));
+          s[mt][nt][2] = fmaf(fb.x, acc[2], fmaf(tb, q.sum[nt][g][0], s[mt][nt][2]));
+          s[mt][nt][3] = fmaf(fb.x, acc[3], fmaf(tb, q.sum[nt][g][1], s[mt][nt][3]));
+        }
+      }
+    }
+    // scores in the log2 domain, hidden ones -inf
+#pragma unroll
+    for (int mt = 0; mt < C::TM; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[mt][nt][e] * q.factor[nt][e & 1];
+          if (masked) {
+            const int tp = pos0 + mt * 16 + t + (e >> 1) * 8, rp = q.pos[nt][e & 1];
+            if (tp > rp || (window > 0 && tp <= rp - window) || !((ok >> mt) & 1)) x = kNegInf;
+          }
+          s[mt][nt][e] = x;
+        }
+    bool moved = false;
+    float corr[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float mx = fmaxf(s[0][nt][k], s[0][nt][2 + k]);
+#pragma unroll
+        for (int mt = 1; mt < C::TM; ++mt) mx = fmaxf(mx, fmaxf(s[mt][nt][k], s[mt][nt][2 + k]));
+#pragma unroll
+        for (int o2 = 4; o2 < 32; o2 *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
+        const float mn = fmaxf(m[nt][k], mx);
+        const float use = mn == kNegInf ? 0.0f : mn;   // nothing seen yet: the weights below are 2^-inf = 0
+        corr[nt][k] = ex2(m[nt][k] - use);
+        moved |= mn != m[nt][k];
+        m[nt][k] = mn;
+#pragma unroll
+        for (int mt = 0; mt < C::TM; ++mt) {
+          s[mt][nt][k] = ex2(s[mt][nt][k] - use);
+          s[mt][nt][2 + k] = ex2(s[mt][nt][2 + k] - use);
+        }
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] *= corr[nt][0];
+        l[nt][1] *= corr[nt][1];
+#pragma unroll
+        for (int j = 0; j < C::J; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] *= corr[nt][e & 1];
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < C::TM; ++mt) {
+      uint32_t b[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt][0] += s[mt][nt][0] + s[mt][nt][2];
+        l[nt][1] += s[mt][nt][1] + s[mt][nt][3];
+        b[nt][0] = movmatrix(h2u(__floats2half2_rn(s[mt][nt][0], s[mt][nt][1])));
+        b[nt][1] = movmatrix(h2u(__floats2half2_rn(s[mt][nt][2], s[mt][nt][3])));
+      }
+      // the lane's tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: rows cc, cc + 8, cc + 4, cc + 12
+      const uint8_t* ch = st + mt * chunk_bytes(D) + 10 * D;
+      uint32_t w[4][C::J], pr[4][C::J];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = cc + (i & 1) * 8 + (i >> 1) * 4;
+        if constexpr (D == 256) lds<C::J>(w[i], ch + row * 128 + ((t ^ ((row & 3) << 1)) * 16));
+        else lds<C::J>(w[i], ch + row * (D / 2) + t * (D / 16));
+        lds<C::J>(pr[i], ch + 8 * D + row * (D / 8) + (t >> 2) * (D / 16));
+        if (masked) {   // rows behind the context may hold anything: 0 times it has to be 0
+          const int tp = pos0 + mt * 16 + 2 * cc + (i & 1) + (i >> 1) * 8;
+          if (tp >= end) {
+#pragma unroll
+            for (int j = 0; j < C::J; ++j) pr[i][j] = 0;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < C::J; ++j) {
+        const uint32_t xl = __byte_perm(w[0][j], w[1][j], 0x5410), xh = __byte_perm(w[0][j], w[1][j], 0x7632);
+        const uint32_t yl = __byte_perm(w[2][j], w[3][j], 0x5410), yh = __byte_perm(w[2][j], w[3][j], 0x7632);
+        const __half2 sx = u2h(__byte_perm(pr[0][j], pr[1][j], 0x5410)), bx = u2h(__byte_perm(pr[0][j], pr[1][j], 0x7632));
+        const __half2 sy = u2h(__byte_perm(pr[2][j], pr[3][j], 0x5410)), by = u2h(__byte_perm(pr[2][j], pr[3][j], 0x7632));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          // nibble e of both halves: 1024 + c in place 0 (0x6400), 64 + c in place 1 (0x5400)
+          const int sh = e & 2 ? 8 : 0;
+          const uint32_t mask = e & 1 ? 0x00f000f0u : 0x000f000fu, magic = e & 1 ? 0x54005400u : 0x64006400u;
+          const __half2 off = e & 1 ? __half2half2(__ushort_as_half(0xd480)) : __half2half2(__ushort_as_half(0xe408));  // -72, -1032
+          const __half2 c0 = __hadd2(u2h(((xl >> sh) & mask) | magic), off);
+          const __half2 c1 = __hadd2(u2h(((xh >> sh) & mask) | magic), off);
+          const __half2 c2 = __hadd2(u2h(((yl >> sh) & mask) | magic), off);
+          const __half2 c3 = __hadd2(u2h(((yh >> sh) & mask) | magic), off);
+          const uint32_t a0 = h2u(__hfma2(c0, sx, bx)), a1 = h2u(__hfma2(c1, sx, bx));
+          const uint32_t a2 = h2u(__hfma2(c2, sy, by)), a3 = h2u(__hfma2(c3, sy, by));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][j][e], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+        }
+      }
+    }
+  }
+
+  // [register][lane] floats
+  __device__ void store(float* f, int lane) const {
+    int r = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < C::J; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) f[(r++) * 32 + lane] = o[nt][j][e / 4][e % 4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      f[(r++) * 32 + lane] = m[nt][0];
+      f[(r++) * 32 + lane] = m[nt][1];
+      f[(r++) * 32 + lane] = l[nt][0];
+      f[(r++) * 32 + lane] = l[nt][1];
+    }
+  }
+};
+
+// Writes 8 numbers (dims 8 w ..) of column k of row block nt, and with w == 0 the row's lse.
+template <int D, int NT>
+__device__ __forceinline__ void write_row(const CacheAttnParams& p, const Cursor& c, int nt, int k, int w, const float (&x)[8],
+                                          float m, float l, int lane) {
+  const int row = c.rt * Cfg<D, NT>::R + nt * 8 + (lane & 3) * 2 + k;
+  if (row >= c.rows * p.group) return;
+  const size_t at = static_cast<size_t>(c.row0 + row / p.group) * p.q_heads + c.h * p.group + row % p.group;
+  const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // nothing seen: 0; NaN stays
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float a = x[2 * e] * inv, b = x[2 * e + 1] * inv;
+    if (p.bf16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+      r[e] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      r[e] = h2u(__floats2half2_rn(a, b));
+    }
+  }
+  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + 8 * w) = make_uint4(r[0], r[1], r[2], r[3]);
+  if (p.lse != nullptr && w == 0) p.lse[at] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
+}
+
+// Joins `n` partial results of an item (addresses from `at(i)`, in the order of their tiles) for
+// one block of registers: row block nt, word j, column k (8 numbers of one row per lane).
+template <int D, int NT, typename At>
+__device__ __forceinline__ void join(int n, const At& at, int nt, int j, int k, int lane, float (&x)[8], float& m,
+                                     float& l) {
+  using C = Cfg<D, NT>;
+  const int mr = C::OREG + nt * 4 + k;
+  m = kNegInf;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[mr * 32 + lane]);
+  const float use = m == kNegInf ? 0.0f : m;
+  l = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float* f = at(i);
+    const float wgt = ex2(f[mr * 32 + lane] - use);
+    l = fmaf(wgt, f[(mr + 2) * 32 + lane], l);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = (nt * C::J + j) * 16 + e * 4 + k;
+      x[e] = fmaf(wgt, f[r * 32 + lane], x[e]);               // dim 8 w + e
+      x[4 + e] = fmaf(wgt, f[(r + 2) * 32 + lane], x[4 + e]); // dim 8 w + 4 + e
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = Cfg<D, NT>;
+  extern __shared__ __align__(16) uint8_t raw[];
+  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(raw);
+  long long* prefix = reinterpret_cast<long long*>(raw + sizeof(Shared<D, NT>));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const Worker<D, NT> wk{p, prefix, lane};
+
+  // tile counts of all sequences, prefix-summed
+  if (tid == 0) sh.scan_total = 0;
+  for (int base = 0; base < p.st.n_seqs; base += C::NW * 32) {
+    const int i = base + tid;
+    long long n = 0;
+    if (i < p.st.n_seqs) {
+      Cursor c;
+      wk.seq(c, i);
+      n = static_cast<long long>(c.tiles) * c.rts * p.st.heads;
+    }
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    long long* wsum = reinterpret_cast<long long*>(sh.meta);   // not in use yet
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    long long before = sh.scan_total;
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (i < p.st.n_seqs) prefix[i] = before + inc - n;
+    __syncthreads();
+    if (tid == C::NW * 32 - 1) sh.scan_total = before + inc;
+    __syncthreads();
+  }
+  const long long T = sh.scan_total;
+  if (tid == 0) prefix[p.st.n_seqs] = T;
+  if (tid < 2 * C::NW) sh.meta[tid].id = -1;
+  __syncthreads();
+
+  // rows that see nothing, and the step's errors
+  for (int i = blockIdx.x; i < p.st.n_seqs; i += gridDim.x) {
+    const SeqSpan s = seq_span(p.st, i);
+    if (s.bad && tid == 0) atomicOr(p.st.err, kErrRange);
+    if (s.live || s.rows == 0) continue;
+    const size_t n = static_cast<size_t>(s.rows) * p.q_heads, at = static_cast<size_t>(s.row0) * p.q_heads;
+    for (size_t e = tid; e < n * (D / 8); e += C::NW * 32)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + e * 8) = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (size_t e = tid; e < n; e += C::NW * 32) p.lse[at + e] = kNegInf;
+  }
+
+  const long long n = T < gridDim.x ? T : gridDim.x;   // CTAs with work
+  if (blockIdx.x >= n) return;
+  const long long c0 = T * blockIdx.x / n, c1 = T * (blockIdx.x + 1) / n;
+  const long long w0 = c0 + (c1 - c0) * warp / C::NW, w1 = c0 + (c1 - c0) * (warp + 1) / C::NW;
+
+  if (w0 < w1) {
+    Cursor c, ahead;
+    wk.seek(c, w0);
+    ahead = c;
+    long long asked = w0;
+    uint32_t ok[C::ST];
+    const uint32_t stage0 = smem_u32(sh.stage[warp][0]);
+    auto ask = [&](int slot) -> uint32_t {
+      uint32_t r = 0;
+      if (asked < w1) {
+        r = wk.request(ahead, stage0 + slot * kTileBytes5k);
+        ++asked;
+        if (++ahead.t == ahead.tiles && asked < w1) wk.next_item(ahead);
+      }
+      cp_async_commit();
+      return r;
+    };
+#pragma unroll
+    for (int s = 0; s < C::ST; ++s) ok[s] = ask(s);
+    Rows<D, NT> q;
+    State<D, NT> st;
+    long long item = w0 - c.t;       // number of the item's first tile
+    bool first = true;
+    int seg0 = c.t;
+    q.load(p, c, lane);
+    st.clear();
+    int slot = 0;
+    for (long long at = w0; at < w1; ++at) {
+      cp_async_wait<C::ST - 1>();
+      __syncwarp();
+      const int pos0 = c.first + c.t * C::TILE;
+      uint32_t have = ok[0];
+#pragma unroll
+      for (int s = 1; s < C::ST; ++s)
+        if (slot == s) have = ok[s];
+      const bool masked = have != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest ||
+                          (p.window > 0 && pos0 <= q.highest - p.window);
+      st.tile(q, sh.stage[warp][slot], pos0, c.end, have, masked, p.window, lane);
+      __syncwarp();
+      const uint32_t r = ask(slot);
+#pragma unroll
+      for (int s = 0; s < C::ST; ++s)
+        if (slot == s) ok[s] = r;
+      slot = slot + 1 == C::ST ? 0 : slot + 1;
+      ++c.t;
+      if (c.t == c.tiles || at + 1 == w1) {
+        st.reduce();
+        if (seg0 == 0 && c.t == c.tiles) {   // the whole item was this warp's
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < C::J; ++j)
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[e] = st.o[nt][j][e][k];
+                  x[4 + e] = st.o[nt][j][e][2 + k];
+                }
+                write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, st.m[nt][k], st.l[nt][k], lane);
+              }
+        } else {
+          float* f = reinterpret_cast<float*>(first ? sh.frag[warp] : sh.stage[warp][0]);
+          if (!first) {                      // the run's last item: its stages are free now
+            cp_async_wait<0>();
+            __syncwarp();
+          }
+          st.store(f, lane);
+          if (lane == 0) sh.meta[2 * warp + (first ? 0 : 1)] = FragMeta{item, c.tiles, c.seq, c.h, c.rt};
+        }
+        first = false;
+        if (at + 1 < w1) {
+          wk.next_item(c);
+          item = at + 1;
+          seg0 = 0;
+          q.load(p, c, lane);
+          st.clear();
+        }
+      }
+    }
+    cp_async_wait<0>();
+  }
+  __syncthreads();
+
+  // Join what warps share; of what CTAs share write this CTA's part.
+  constexpr int kUnits = NT * C::J * 2;
+  auto slot_at = [&](int s) -> const float* {
+    return reinterpret_cast<const float*>(s & 1 ? sh.stage[s >> 1][0] : sh.frag[s >> 1]);
+  };
+  auto cta_of = [&](long long tile) { return static_cast<int>(((tile + 1) * n - 1) / T); };
+  int shared_items = 0;
+  for (int s = 0; s < 2 * C::NW; ++s) {
+    const FragMeta fm = sh.meta[s];
+    if (fm.id < 0) continue;
+    int list[2 * C::NW], cntf = 0, e = s;
+    for (; e < 2 * C::NW; ++e) {
+      if (sh.meta[e].id < 0) continue;
+      if (sh.meta[e].id != fm.id) break;
+      list[cntf++] = e;
+    }
+    const bool whole = fm.id >= c0 && fm.id + fm.tiles <= c1;
+    Cursor c;
+    wk.seq(c, fm.seq);
+    c.h = fm.h;
+    c.rt = fm.rt;
+    const int out_slot = fm.id >= c0 ? 1 : 0;
+    float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + out_slot) * (C::FREG * 32);
+    for (int u = warp; u < kUnits; u += C::NW) {
+      const int k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
+      float x[8], m, l;
+      join<D, NT>(cntf, [&](int i) { return slot_at(list[i]); }, nt, j, k, lane, x, m, l);
+      if (whole) {
+        write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
+      } else {
+#pragma unroll
+        for (int e2 = 0; e2 < 4; ++e2) {
+          const int r = (nt * C::J + j) * 16 + e2 * 4 + k;
+          part[r * 32 + lane] = x[e2];
+          part[(r + 2) * 32 + lane] = x[4 + e2];
+        }
+        if (j == 0) {
+          part[(C::OREG + nt * 4 + k) * 32 + lane] = m;
+          part[(C::OREG + nt * 4 + 2 + k) * 32 + lane] = l;
+        }
+      }
+    }
+    if (!whole) ++shared_items;
+    s = e - 1;
+  }
+  if (shared_items == 0) return;
+
+  // Count this CTA's parts; the CTA that counts an item's last one adds them up.
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) sh.last[tid] = 0;
+  __syncthreads();
+  long long ids[2] = {-1, -1};
+  int which[2] = {0, 0}, items = 0;
+  for (int s = 0; s < 2 * C::NW; ++s) {
+    const long long id = sh.meta[s].id;
+    if (id < 0 || (id >= c0 && id + sh.meta[s].tiles <= c1) || (items > 0 && ids[items - 1] == id)) continue;
+    if (items < 2) {
+      ids[items] = id;
+      which[items++] = s;
+    }
+  }
+  if (tid < items) {
+    const FragMeta fm = sh.meta[which[tid]];
+    const int f0 = cta_of(fm.id), f1 = cta_of(fm.id + fm.tiles - 1);
+    const uint32_t seen = atom_add_acq_rel_gpu(p.cnt + f0, 1u);
+    if (seen == static_cast<uint32_t>(f1 - f0)) {
+      sh.last[tid] = 1;
+      p.cnt[f0] = 0;          // as the next call needs it; nobody else touches it any more
+    }
+  }
+  __syncthreads();
+  for (int it = 0; it < items; ++it) {
+    if (!sh.last[it]) continue;
+    const FragMeta fm = sh.meta[which[it]];
+    const int f0 = cta_of(fm.id), f1 = cta_of(fm.id + fm.tiles - 1);
+    Cursor c;
+    wk.seq(c, fm.seq);
+    c.h = fm.h;
+    c.rt = fm.rt;
+    for (int u = warp; u < kUnits; u += C::NW) {
+      const int k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
+      float x[8], m, l;
+      join<D, NT>(f1 - f0 + 1,
+                  [&](int i) { return static_cast<const float*>(p.part + static_cast<size_t>((f0 + i) * 2 + (i == 0 ? 1 : 0)) * (C::FREG * 32)); },
+                  nt, j, k, lane, x, m, l);
+      write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
+    }
+  }
+}
+
+template <int D, int NT>
+cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
+  const size_t smem = sizeof(Shared<D, NT>) + (static_cast<size_t>(p.st.n_seqs) + 1) * 8;
+  const cudaError_t e =
+      cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(sizeof(Shared<D, NT>) + (kCacheMaxSeqs + 1) * 8));
+  if (e != cudaSuccess) return e;
+  cache_attention_kernel<D, NT><<<p.grid, Cfg<D, NT>::NW * 32, smem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
+  CacheAttnWs w{};
+  const int nt = rows > 8 && dim <= 128 ? 2 : 1;
+  const size_t regs = static_cast<size_t>(nt) * (dim / 64) * 16 + 4 * nt;
+  w.cnt = 0;
+  w.part = (static_cast<size_t>(sms) * 4 + 255) / 256 * 256;
+  w.total = w.part + static_cast<size_t>(sms) * 2 * regs * 128;
+  return w;
+}
+
+// Rows of an item: 8, or 16 where a head has more than 8 (the packed bytes are then
+// unpacked half as often); D = 256 keeps 8, whose accumulators are 64 registers already.
+cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream) {
+  if (dim == 64) return rows > 8 ? launch_as<64, 2>(p, stream) : launch_as<64, 1>(p, stream);
+  if (dim == 128) return rows > 8 ? launch_as<128, 2>(p, stream) : launch_as<128, 1>(p, stream);
+  return launch_as<256, 1>(p, stream);
+}
+
+}  // namespace bs
