@@ -75,7 +75,7 @@ struct CacheAttnParams {
   const void* q;
   long long q_tok, q_head;           // strides in elements
   int q_heads, group;
-  int bf16, window;
+  int bf16, window;                  // window: 2^31 - 1 when unlimited
   float scale_log2;                  // scale * log2(e): scores are kept in the log2 domain
   void* out;
   float* lse;

@@ -189,7 +189,7 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
   p.q_heads = q_heads;
   p.group = q_heads / cache->heads;
   p.bf16 = dt == BS_BF16 ? 1 : 0;
-  p.window = window;
+  p.window = window == 0 ? 0x7fffffff : window;   // positions are below it
   p.scale_log2 = scale * 1.4426950408889634f;
   p.out = out;
   p.lse = lse;

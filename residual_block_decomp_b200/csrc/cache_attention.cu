@@ -15,26 +15,27 @@
 // warps share is joined in shared memory, of items that several CTAs share in the workspace by the CTA
 // that arrives last; both add in the order of the tiles, so results do not depend on timing.
 //
-// Products.  Tokens are the M side of mma.m16n8k16 and query rows its N side (8 rows: the
-// heads that share a key/value head), so few rows waste little.  tcgen05 would need 128
-// rows of queries or would take the keys through shared memory as dense operands; here
-// the codes go from their packed words to fragments in registers.
-//  * Keys: a lane's words give the fragments of its tokens directly: (word >> s) & 0x00f000f0
-//    | 0x5400 is the pair 64 + c in fp16, exact.  Per group of 32: acc = sum (64 + c) q, and with
-//    the token's pair (s, b): s acc + (b - 72 s) sum q = sum (b + s (c - 8)) q, in fp32.  No per-number
-//    arithmetic is needed, and a code's product with q is exact.
-//  * Softmax: the accumulator layout holds rows = tokens, columns = query rows; the maximum over tokens
-//    is three shuffles, and movmatrix turns the fp16 weights into the next product's
-//    B fragment.
+// Products.  Tokens are the M side of mma.sync and query rows its N side (8 rows: the heads that share a
+// key/value head), so few rows waste little.  tcgen05 would need 128 rows of queries or would take the
+// keys through shared memory as dense operands; here the codes go from their packed words to fragments in
+// registers.
+//  * Keys: (word >> s) & 0x00f000f0 | 0x5400 is a pair of codes as the exact fp16 numbers 64 + c. Per group of
+//    32, acc = sum (64 + c) q, and a token's score is the sum over groups of s acc + (b - 72 s) sum q; the
+//    second part is one product of the (s, b) pairs as they are stored with (-72 sum, sum), each in two fp16
+//    parts (22 bits).  So the scales of keys cost one fp32 fma a group and score, none a number.
+//    A query row enters as fp16, scaled by a power of two to have its largest entry in [1, 2) (undone in
+//    the fp32 scores): exact down to 2^-14 of that entry (bf16: 2^-17), and within 2^-25 of it below.
+//  * Softmax: the accumulator layout holds rows = tokens, columns = query rows.  The reference m of the weights
+//    2^(x - m) follows the running maximum only when a score passes it by more than 8 (weights stay below 2^8,
+//    far inside fp16): most tiles then need no shuffles and no rescaling, only a vote.
+//    movmatrix turns the fp16 weights into the next product's B fragment.
 //  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
 //    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).
 //    Scales cannot stay outside the product here as for keys: the token is what is summed over.
-//
-// Queries are taken as fp16.  fp16 inputs are exact; a bf16 row is first scaled by a power of two that
-// brings its largest entry into [1, 2) (undone in the fp32 scores): exact down to
-// 2^-14 of that entry, and within 2^-25 of it below.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <atomic>
 
 #include "cache.h"
 #include "ptx.cuh"
@@ -44,6 +45,8 @@ namespace {
 
 constexpr int kTileBytes5k = 5120;
 constexpr float kNegInf = -INFINITY;
+constexpr float kNothing = -3.0e38f;   // the reference before any score
+constexpr float kLag = 8.0f;           // how far scores may pass it
 
 template <int D, int NT>
 struct Cfg {
@@ -57,6 +60,7 @@ struct Cfg {
   static constexpr int FBYTES = FREG * 128;                   // a warp's partial result
   static constexpr int NW = (NT == 1 && D <= 128) ? 12 : 8;   // warps
   static constexpr int ST = 2;                                // stages of a warp
+  static constexpr int UC = chunk_bytes(D) / 16;              // 16-byte units of a chunk
 };
 
 // Partial results are laid out [register][lane].
@@ -82,11 +86,13 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, bool fill) {
-  const int n = fill ? 16 : 0;
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// (word & 0x00f000f0) | 0x54005400: nibbles 1 and 5 of a word as the fp16 pair 64 + c.
+// (w & 0x00f000f0) | 0x54005400: nibbles 1 and 5 of a word as the fp16 pair 64 + c.
 __device__ __forceinline__ uint32_t pair64(uint32_t w) { return (w & 0x00f000f0u) | 0x54005400u; }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -111,6 +117,13 @@ __device__ __forceinline__ void lds(uint32_t (&r)[N], const uint8_t* p) {
 struct Cursor {
   int seq, h, rt, t, tiles, rts, first;   // first: the position the item's tiles begin at (a multiple of 16)
   int row0, rows, start, end;             // the sequence's rows and positions; end: positions seen
+};
+// Where the copies of a warp's run stand: the next chunk's address inside its page, and the table's entries
+// for the pages 32 k .. 32 k + 31 of a sequence, one a lane.
+struct Feed {
+  const uint8_t* next;   // this lane's 16 bytes of the next chunk
+  bool good;             // its page is in the pool
+  int seq, block, page;
 };
 
 template <int D, int NT>
@@ -144,7 +157,7 @@ struct Worker {
     c.tiles = 0;
     c.rts = 0;
     if (!s.live) return;
-    if (p.window > 0 && s.start >= p.window) c.first = (s.start - p.window + 1) / kChunkTokens * kChunkTokens;
+    if (s.start >= p.window) c.first = (s.start - p.window + 1) / kChunkTokens * kChunkTokens;
     c.tiles = (c.end - c.first + C::TILE - 1) / C::TILE;
     c.rts = (s.rows * p.group + C::R - 1) / C::R;
   }
@@ -173,57 +186,84 @@ struct Worker {
     if (i < p.st.n_seqs) seq(c, i);
   }
 
+  // 5120 bytes from the tile's chunks; chunks that are not there (ALL false) become zeros.
+  template <bool ALL>
+  __device__ __forceinline__ void copy(const uint8_t* const (&src)[C::TM], uint32_t ok, uint32_t stage) const {
+    auto one = [&](uint32_t dst, const uint8_t* from, int m) {
+      if (ALL) {
+        cp16(dst, from);
+      } else {
+        const bool there = (ok >> m) & 1;
+        cp16_zfill(dst, there ? from : p.st.pages, there ? 16 : 0);
+      }
+    };
+    const uint32_t dst = stage + lane * 16;
+    if constexpr (D == 64) {
+      // two chunks are 160 units: 5 copies a lane, the third astride
+#pragma unroll
+      for (int m = 0; m < C::TM; m += 2) {
+        const bool second = lane >= 16;
+        one(dst + m * chunk_bytes(D), src[m], m);
+        one(dst + m * chunk_bytes(D) + 512, src[m] + 512, m);
+        one(dst + m * chunk_bytes(D) + 1024, second ? src[m + 1] + (1024 - chunk_bytes(D)) : src[m] + 1024, second ? m + 1 : m);
+        one(dst + m * chunk_bytes(D) + 1536, src[m + 1] + (1536 - chunk_bytes(D)), m + 1);
+        one(dst + m * chunk_bytes(D) + 2048, src[m + 1] + (2048 - chunk_bytes(D)), m + 1);
+      }
+    } else if constexpr (D == 128) {
+#pragma unroll
+      for (int m = 0; m < C::TM; ++m)
+#pragma unroll
+        for (int k = 0; k < 5; ++k) one(dst + m * chunk_bytes(D) + k * 512, src[m] + k * 512, m);
+    } else {
+      // rows of 128 bytes: the lanes' units are spread over the banks
+      const uint32_t dk = stage + (lane ^ ((lane >> 3) & 1)) * 16, dv = stage + (lane ^ ((lane >> 3) << 1)) * 16;
+#pragma unroll
+      for (int k = 0; k < 10; ++k) one((k < 4 ? dk : (k > 4 && k < 9) ? dv : dst) + k * 512, src[0] + k * 512, 0);
+    }
+  }
+
   // Requests tile c.t of the item into `stage`; returns which of its chunks are in the pool.
-  __device__ uint32_t request(const Cursor& c, uint32_t stage) const {
+  __device__ uint32_t request(const Cursor& c, Feed& fd, uint32_t stage) const {
     const uint8_t* src[C::TM];
     uint32_t ok = 0;
+    const int pos0 = c.first + c.t * C::TILE, shift = p.st.page_shift;
 #pragma unroll
     for (int m = 0; m < C::TM; ++m) {
-      const int pos = c.first + c.t * C::TILE + m * kChunkTokens;
-      src[m] = nullptr;
-      if (pos < c.end) {
-        const int page = __ldg(p.st.table + static_cast<size_t>(c.seq) * p.st.stride + (pos >> p.st.page_shift));
-        src[m] = chunk_at(p.st, page, pos, c.h, D);
-        if (src[m] != nullptr) ok |= 1u << m;
-        else if (lane == 0) atomicOr(p.st.err, kErrRange);
+      const int pos = pos0 + m * kChunkTokens;
+      if ((pos & ((1 << shift) - 1)) == 0 || (m == 0 && (c.t == 0 || fd.seq < 0))) {   // a new page, item or run
+        const int idx = pos >> shift;
+        if (fd.seq != c.seq || fd.block != idx >> 5) {
+          fd.seq = c.seq;
+          fd.block = idx >> 5;
+          const int mine = (fd.block << 5) + lane;
+          fd.page = mine <= (c.end - 1) >> shift ? __ldg(p.st.table + static_cast<size_t>(c.seq) * p.st.stride + mine) : 0;
+        }
+        const uint32_t page = __shfl_sync(0xffffffffu, fd.page, idx & 31);
+        const int in_page = (1 << shift) / kChunkTokens;
+        const uint32_t chunk = c.h * in_page + ((pos / kChunkTokens) & (in_page - 1));
+        fd.good = page < static_cast<uint32_t>(p.st.n_pages);
+        fd.next = p.st.pages + lane * 16 + chunk * chunk_bytes(D);
+        if (fd.good) fd.next += static_cast<unsigned long long>(page) * static_cast<uint32_t>(p.st.page_bytes);
+        else if (pos < c.end && lane == 0) atomicOr(p.st.err, kErrRange);
       }
+      src[m] = fd.next;
+      fd.next += chunk_bytes(D);
+      if (fd.good && pos < c.end) ok |= 1u << m;
     }
-    constexpr int UC = chunk_bytes(D) / 16;   // 16-byte units of a chunk
-#pragma unroll
-    for (int k = 0; k < kTileBytes5k / 512; ++k) {
-      const int u = k * 32 + lane;
-      int m, o;                               // chunk, and unit inside it
-      if constexpr (D == 64) {
-        const int half = k / 5;               // 160 units: two chunks
-        const int v = u - half * 160;
-        m = 2 * half + (v >= UC ? 1 : 0);
-        o = v >= UC ? v - UC : v;
-      } else {
-        m = k / (UC / 32);
-        o = u - m * UC;
-      }
-      const uint8_t* base = src[0];
-#pragma unroll
-      for (int i = 1; i < C::TM; ++i)
-        if (m == i) base = src[i];
-      int d = o;
-      if constexpr (D == 256) {               // rows of 128 bytes: spread the lanes' units over the banks
-        if (o < 128) d = o ^ ((o >> 3) & 1);
-        else if (o >= 160 && o < 288) d = o ^ ((((o - 160) >> 3) & 3) << 1);
-      }
-      cp16_zfill(stage + (m * UC + d) * 16, base == nullptr ? p.st.pages : base + o * 16, base != nullptr);
-    }
+    if (ok == (1u << C::TM) - 1) copy<true>(src, ok, stage);
+    else copy<false>(src, ok, stage);
     return ok;
   }
 };
 
-// The rows of an item as a lane needs them: query fragments (its row's numbers), and for
-// the accumulator columns 2 (lane % 4) + {0, 1}: sums over groups, score factors, positions.
+// The rows of an item as a lane needs them: query fragments (its row's numbers), the sums over groups as the
+// operand of the pairs' product, and for the accumulator columns 2 (lane % 4) + {0, 1} score factors and
+// positions.
 template <int D, int NT>
 struct Rows {
   using C = Cfg<D, NT>;
   uint32_t q[NT][C::GR][4];
-  float sum[NT][C::GR][2];
+  uint32_t sums[NT][C::GR > 4 ? 2 : 1][2];
   float factor[NT][2];
   int pos[NT][2];        // position of the row's token; -1: no such row
   int lowest, highest;   // positions of the item's first and last row
@@ -243,56 +283,69 @@ struct Rows {
 #pragma unroll
       for (int gr = 0; gr < C::GR; ++gr)
         raw[gr] = row < total ? __ldg(reinterpret_cast<const uint4*>(src + gr * 32)) : make_uint4(0, 0, 0, 0);
-      float back = 1.0f;
-      if (p.bf16) {
-        uint32_t top = 0;   // exponent bits of the row's largest entry
-#pragma unroll
-        for (int gr = 0; gr < C::GR; ++gr) {
-          const uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = max(top, max(r[e] & 0x7f800000u, (r[e] << 16) & 0x7f800000u));
-        }
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^-e for a finite normal exponent e below 127; inf and NaN rows, and rows of zeros and
-        // subnormals, are taken unscaled or by the smallest normal
-        uint32_t up = 254u << 23;
-        float scale = 1.0f;
-        if (top != 0x7f800000u) {
-          if (top == 0) top = 1u << 23;
-          back = __uint_as_float(top);
-          scale = __uint_as_float(up - top);
-          if (top == up) scale = 0x1p-127f;   // e = 127: 2^-127, a subnormal factor, exact
-        }
-#pragma unroll
-        for (int gr = 0; gr < C::GR; ++gr) {
-          uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float lo = __uint_as_float(r[e] << 16) * scale, hi = __uint_as_float(r[e] & 0xffff0000u) * scale;
-            r[e] = h2u(__floats2half2_rn(lo, hi));
-          }
-          raw[gr] = make_uint4(r[0], r[1], r[2], r[3]);
-        }
-      }
-      const float f = p.scale_log2 * back;
+      auto two = [&](uint32_t r) {   // two numbers in fp32
+        return p.bf16 ? make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u)) : __half22float2(u2h(r));
+      };
+      uint32_t top = 0;              // exponent bits of the row's largest entry
 #pragma unroll
       for (int gr = 0; gr < C::GR; ++gr) {
-        // numbers (d, d + 4) pair up as the codes of a word do
-        q[nt][gr][0] = __byte_perm(raw[gr].x, raw[gr].z, 0x5410);
-        q[nt][gr][1] = __byte_perm(raw[gr].x, raw[gr].z, 0x7632);
-        q[nt][gr][2] = __byte_perm(raw[gr].y, raw[gr].w, 0x5410);
-        q[nt][gr][3] = __byte_perm(raw[gr].y, raw[gr].w, 0x7632);
+        const uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = two(r[e]);
+          top = max(top, max(__float_as_uint(v.x) & 0x7f800000u, __float_as_uint(v.y) & 0x7f800000u));
+        }
+      }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const int ex = static_cast<int>(top >> 23);
+      // 2^(127 - ex) as far as that is a normal float; the scale's sign goes with it, so that factors are positive
+      const int up = min(max(254 - ex, 1), 254);
+      float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
+      float f = ldexpf(fabsf(p.scale_log2), 127 - up);
+      f = fmaxf(f, 0x1p-120f);                           // 0 times a hidden score of -inf would be NaN
+      if (ex == 255) {                                   // a row with inf or NaN is NaN
+        f = __int_as_float(0x7fffffff);
+        scale = 0.0f;
+      }
+      if (p.scale_log2 < 0.0f) scale = -scale;
+      if (p.scale_log2 == 0.0f) scale = 0.0f;
+      float sum[C::GR];
+#pragma unroll
+      for (int gr = 0; gr < C::GR; ++gr) {
+        uint32_t r[4] = {raw[gr].x, raw[gr].y, raw[gr].z, raw[gr].w};
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 v = __half22float2(u2h(q[nt][gr][e]));
-          s += v.x + v.y;
+          const float2 v = two(r[e]);
+          const __half2 h = ex == 255 ? __floats2half2_rn(0.0f, 0.0f) : __floats2half2_rn(v.x * scale, v.y * scale);
+          const float2 back = __half22float2(h);
+          s += back.x + back.y;
+          r[e] = h2u(h);
         }
+        // numbers (d, d + 4) pair up as the codes of a word do
+        q[nt][gr][0] = __byte_perm(r[0], r[2], 0x5410);
+        q[nt][gr][1] = __byte_perm(r[0], r[2], 0x7632);
+        q[nt][gr][2] = __byte_perm(r[1], r[3], 0x5410);
+        q[nt][gr][3] = __byte_perm(r[1], r[3], 0x7632);
         s += __shfl_xor_sync(0xffffffffu, s, 1);
         s += __shfl_xor_sync(0xffffffffu, s, 2);
-        sum[nt][gr][0] = __shfl_sync(0xffffffffu, s, 8 * cc);
-        sum[nt][gr][1] = __shfl_sync(0xffffffffu, s, 8 * cc + 4);
+        sum[gr] = s;
+      }
+      // the pairs' operand: k = 2 cc, 2 cc + 1 meet (s, b) of group cc, the second k half holds what fp16
+      // leaves of the sums (D = 64: lanes cc >= 2 of the first half do)
+#pragma unroll
+      for (int k = 0; k < (C::GR > 4 ? 2 : 1); ++k) {
+        float v = sum[k * 4];
+#pragma unroll
+        for (int gr = 1; gr < (C::GR < 4 ? C::GR : 4); ++gr)
+          if ((C::GR < 4 ? cc & 1 : cc) == gr) v = sum[k * 4 + gr];
+        const float w = -72.0f * v;
+        const __half2 hi = __floats2half2_rn(w, v);
+        const float2 hf = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(w - hf.x, v - hf.y);
+        sums[nt][k][0] = h2u(C::GR < 4 && cc >= 2 ? lo : hi);
+        sums[nt][k][1] = C::GR < 4 ? 0 : h2u(lo);
       }
       const int at = row < total ? c.start + i : -1;
 #pragma unroll
@@ -309,7 +362,7 @@ template <int D, int NT>
 struct State {
   using C = Cfg<D, NT>;
   float o[NT][C::J][4][4];
-  float m[NT][2], l[NT][2];   // l: this lane's tokens only until reduce()
+  float m[NT][2], l[NT][2];   // m: the weights' reference; l: this lane's tokens only until reduce()
 
   __device__ void clear() {
 #pragma unroll
@@ -318,7 +371,7 @@ struct State {
       for (int j = 0; j < C::J; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] = 0.0f;
-      m[nt][0] = m[nt][1] = kNegInf;
+      m[nt][0] = m[nt][1] = kNothing;
       l[nt][0] = l[nt][1] = 0.0f;
     }
   }
@@ -332,9 +385,17 @@ struct State {
   }
 
   // One tile: positions pos0 .., of which `ok` chunks hold tokens; `masked`: some (row, token) is hidden.
-  __device__ void tile(const Rows<D, NT>& q, const uint8_t* st, int pos0, int end, uint32_t ok, bool masked, int window,
-                       int lane) {
+  __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int end, uint32_t ok, bool masked, int window, int lane) {
     const int t = lane >> 2, cc = lane & 3;
+    if (pos0 + C::TILE > end) {
+      // rows behind the context may hold anything: their values become 0 + 0 (c - 8), as 0 times them has to be 0
+      for (int i = end - pos0 + lane; i < C::TILE; i += 32) {
+        uint32_t* pr = reinterpret_cast<uint32_t*>(st + (i >> 4) * chunk_bytes(D) + 18 * D + (((i & 15) >> 1) + 8 * (i & 1)) * (D / 8));
+#pragma unroll
+        for (int g = 0; g < C::GR; ++g) pr[g] = 0;
+      }
+      __syncwarp();
+    }
     float s[C::TM][NT][4];
 #pragma unroll
     for (int mt = 0; mt < C::TM; ++mt) {
@@ -363,72 +424,79 @@ struct State {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[mt][nt][e] = 0.0f;
 #pragma unroll
+      for (int k = 0; k < (C::GR > 4 ? 2 : 1); ++k) {
+        uint32_t ra[1], rb[1];
+        const int at = 16 * k + (C::GR < 4 ? cc & 1 : cc) * 4;
+        lds<1>(ra, ch + 8 * D + t * (D / 8) + at);
+        lds<1>(rb, ch + 8 * D + (t + 8) * (D / 8) + at);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(s[mt][nt], ra[0], rb[0], ra[0], rb[0], q.sums[nt][k][0], q.sums[nt][k][1]);
+      }
+#pragma unroll
       for (int g = 0; g < C::GR; ++g) {
-        const float2 fa = __half22float2(u2h(pa[g])), fb = __half22float2(u2h(pb[g]));
-        const float ta = fmaf(-72.0f, fa.x, fa.y), tb = fmaf(-72.0f, fb.x, fb.y);
-        const uint32_t a0 = pair64(wa[g] << 4), a1 = pair64(wb[g] << 4);
-        const uint32_t a2 = pair64(wa[g]), a3 = pair64(wb[g]);
-        const uint32_t a4 = pair64(wa[g] >> 4), a5 = pair64(wb[g] >> 4);
-        const uint32_t a6 = pair64(wa[g] >> 8), a7 = pair64(wb[g] >> 8);
+        const float fa = __low2float(u2h(pa[g])), fb = __low2float(u2h(pb[g]));
+        const uint32_t a0 = pair64(wa[g] << 4), a1 = pair64(wb[g] << 4), a2 = pair64(wa[g]), a3 = pair64(wb[g]);
+        const uint32_t a4 = pair64(wa[g] >> 4), a5 = pair64(wb[g] >> 4), a6 = pair64(wa[g] >> 8), a7 = pair64(wb[g] >> 8);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
           mma16816(acc, a0, a1, a2, a3, q.q[nt][g][0], q.q[nt][g][1]);
           mma16816(acc, a4, a5, a6, a7, q.q[nt][g][2], q.q[nt][g][3]);
-          s[mt][nt][0] = fmaf(fa.x, acc[0], fmaf(ta, q.sum[nt][g][0], s[mt][nt][0]));
-          s[mt][nt][1] = fmaf(fa.x, acc[1], fmaf(ta, q.sum[nt][g][1], s[mt][nt][1]));
-          s[mt][nt][2] = fmaf(fb.x, acc[2], fmaf(tb, q.sum[nt][g][0], s[mt][nt][2]));
-          s[mt][nt][3] = fmaf(fb.x, acc[3], fmaf(tb, q.sum[nt][g][1], s[mt][nt][3]));
+          s[mt][nt][0] = fmaf(fa, acc[0], s[mt][nt][0]);
+          s[mt][nt][1] = fmaf(fa, acc[1], s[mt][nt][1]);
+          s[mt][nt][2] = fmaf(fb, acc[2], s[mt][nt][2]);
+          s[mt][nt][3] = fmaf(fb, acc[3], s[mt][nt][3]);
         }
       }
     }
-    // scores in the log2 domain, hidden ones -inf
+    if (masked) {
+#pragma unroll
+      for (int mt = 0; mt < C::TM; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tp = pos0 + mt * 16 + t + (e >> 1) * 8, rp = q.pos[nt][e & 1];
+            if (tp > rp || tp <= rp - window || !((ok >> mt) & 1)) s[mt][nt][e] = kNegInf;
+          }
+    }
+    float mx[NT][2];
+    bool passed = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        mx[nt][k] = fmaxf(s[0][nt][k], s[0][nt][2 + k]);
+#pragma unroll
+        for (int mt = 1; mt < C::TM; ++mt) mx[nt][k] = fmaxf(mx[nt][k], fmaxf(s[mt][nt][k], s[mt][nt][2 + k]));
+        mx[nt][k] *= q.factor[nt][k];
+        passed |= mx[nt][k] > m[nt][k] + kLag;
+      }
+    if (__any_sync(0xffffffffu, passed)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float corr[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+          for (int o2 = 4; o2 < 32; o2 *= 2) mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], o2));
+          const float mn = fmaxf(m[nt][k], mx[nt][k]);
+          corr[k] = ex2(m[nt][k] - mn);
+          m[nt][k] = mn;
+          l[nt][k] *= corr[k];
+        }
+#pragma unroll
+        for (int j = 0; j < C::J; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] *= corr[e & 1];
+      }
+    }
 #pragma unroll
     for (int mt = 0; mt < C::TM; ++mt)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[mt][nt][e] * q.factor[nt][e & 1];
-          if (masked) {
-            const int tp = pos0 + mt * 16 + t + (e >> 1) * 8, rp = q.pos[nt][e & 1];
-            if (tp > rp || (window > 0 && tp <= rp - window) || !((ok >> mt) & 1)) x = kNegInf;
-          }
-          s[mt][nt][e] = x;
-        }
-    bool moved = false;
-    float corr[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        float mx = fmaxf(s[0][nt][k], s[0][nt][2 + k]);
-#pragma unroll
-        for (int mt = 1; mt < C::TM; ++mt) mx = fmaxf(mx, fmaxf(s[mt][nt][k], s[mt][nt][2 + k]));
-#pragma unroll
-        for (int o2 = 4; o2 < 32; o2 *= 2) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o2));
-        const float mn = fmaxf(m[nt][k], mx);
-        const float use = mn == kNegInf ? 0.0f : mn;   // nothing seen yet: the weights below are 2^-inf = 0
-        corr[nt][k] = ex2(m[nt][k] - use);
-        moved |= mn != m[nt][k];
-        m[nt][k] = mn;
-#pragma unroll
-        for (int mt = 0; mt < C::TM; ++mt) {
-          s[mt][nt][k] = ex2(s[mt][nt][k] - use);
-          s[mt][nt][2 + k] = ex2(s[mt][nt][2 + k] - use);
-        }
-      }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] *= corr[nt][0];
-        l[nt][1] *= corr[nt][1];
-#pragma unroll
-        for (int j = 0; j < C::J; ++j)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] *= corr[nt][e & 1];
-      }
-    }
+        for (int e = 0; e < 4; ++e) s[mt][nt][e] = ex2(fmaf(s[mt][nt][e], q.factor[nt][e & 1], -m[nt][e & 1]));
 #pragma unroll
     for (int mt = 0; mt < C::TM; ++mt) {
       uint32_t b[NT][2];
@@ -448,13 +516,6 @@ struct State {
         if constexpr (D == 256) lds<C::J>(w[i], ch + row * 128 + ((t ^ ((row & 3) << 1)) * 16));
         else lds<C::J>(w[i], ch + row * (D / 2) + t * (D / 16));
         lds<C::J>(pr[i], ch + 8 * D + row * (D / 8) + (t >> 2) * (D / 16));
-        if (masked) {   // rows behind the context may hold anything: 0 times it has to be 0
-          const int tp = pos0 + mt * 16 + 2 * cc + (i & 1) + (i >> 1) * 8;
-          if (tp >= end) {
-#pragma unroll
-            for (int j = 0; j < C::J; ++j) pr[i][j] = 0;
-          }
-        }
       }
 #pragma unroll
       for (int j = 0; j < C::J; ++j) {
@@ -530,16 +591,15 @@ __device__ __forceinline__ void join(int n, const At& at, int nt, int j, int k, 
                                      float& l) {
   using C = Cfg<D, NT>;
   const int mr = C::OREG + nt * 4 + k;
-  m = kNegInf;
+  m = kNothing;
   for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[mr * 32 + lane]);
-  const float use = m == kNegInf ? 0.0f : m;
   l = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.0f;
 #pragma unroll 2
   for (int i = 0; i < n; ++i) {
     const float* f = at(i);
-    const float wgt = ex2(f[mr * 32 + lane] - use);
+    const float wgt = ex2(f[mr * 32 + lane] - m);
     l = fmaf(wgt, f[(mr + 2) * 32 + lane], l);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -611,48 +671,45 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     Cursor c, ahead;
     wk.seek(c, w0);
     ahead = c;
-    long long asked = w0;
-    uint32_t ok[C::ST];
+    Feed feed{nullptr, false, -1, 0, 0};
+    int todo = static_cast<int>(w1 - w0), unasked = todo;
+    uint32_t have = 0;                // bits of the requested tiles' chunks, the oldest lowest
     const uint32_t stage0 = smem_u32(sh.stage[warp][0]);
-    auto ask = [&](int slot) -> uint32_t {
+    auto ask = [&](int slot) {
       uint32_t r = 0;
-      if (asked < w1) {
-        r = wk.request(ahead, stage0 + slot * kTileBytes5k);
-        ++asked;
-        if (++ahead.t == ahead.tiles && asked < w1) wk.next_item(ahead);
+      if (unasked > 0) {
+        r = wk.request(ahead, feed, stage0 + slot * kTileBytes5k);
+        --unasked;
+        if (++ahead.t == ahead.tiles && unasked > 0) wk.next_item(ahead);
       }
       cp_async_commit();
-      return r;
+      have = have >> C::TM | r << ((C::ST - 1) * C::TM);
     };
-#pragma unroll
-    for (int s = 0; s < C::ST; ++s) ok[s] = ask(s);
+    for (int s = 0; s < C::ST; ++s) ask(s);
     Rows<D, NT> q;
     State<D, NT> st;
     long long item = w0 - c.t;       // number of the item's first tile
-    bool first = true;
+    bool first = true, fresh = true;
     int seg0 = c.t;
-    q.load(p, c, lane);
-    st.clear();
     int slot = 0;
-    for (long long at = w0; at < w1; ++at) {
+    while (todo > 0) {
+      if (fresh) {
+        q.load(p, c, lane);
+        st.clear();
+        fresh = false;
+      }
       cp_async_wait<C::ST - 1>();
       __syncwarp();
       const int pos0 = c.first + c.t * C::TILE;
-      uint32_t have = ok[0];
-#pragma unroll
-      for (int s = 1; s < C::ST; ++s)
-        if (slot == s) have = ok[s];
-      const bool masked = have != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest ||
-                          (p.window > 0 && pos0 <= q.highest - p.window);
-      st.tile(q, sh.stage[warp][slot], pos0, c.end, have, masked, p.window, lane);
+      const uint32_t ok = have & ((1u << C::TM) - 1);
+      const bool masked = ok != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest || pos0 <= q.highest - p.window;
+      st.tile(q, sh.stage[warp][slot], pos0, c.end, ok, masked, p.window, lane);
       __syncwarp();
-      const uint32_t r = ask(slot);
-#pragma unroll
-      for (int s = 0; s < C::ST; ++s)
-        if (slot == s) ok[s] = r;
+      ask(slot);
       slot = slot + 1 == C::ST ? 0 : slot + 1;
+      --todo;
       ++c.t;
-      if (c.t == c.tiles || at + 1 == w1) {
+      if (c.t == c.tiles || todo == 0) {
         st.reduce();
         if (seg0 == 0 && c.t == c.tiles) {   // the whole item was this warp's
 #pragma unroll
@@ -679,12 +736,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
           if (lane == 0) sh.meta[2 * warp + (first ? 0 : 1)] = FragMeta{item, c.tiles, c.seq, c.h, c.rt};
         }
         first = false;
-        if (at + 1 < w1) {
+        if (todo > 0) {
           wk.next_item(c);
-          item = at + 1;
+          item = w1 - todo;
           seg0 = 0;
-          q.load(p, c, lane);
-          st.clear();
+          fresh = true;
         }
       }
     }
@@ -785,15 +841,22 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
 
 template <int D, int NT>
 cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
-  const size_t smem = sizeof(Shared<D, NT>) + (static_cast<size_t>(p.st.n_seqs) + 1) * 8;
-  const cudaError_t e =
-      cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(sizeof(Shared<D, NT>) + (kCacheMaxSeqs + 1) * 8));
+  constexpr int kMost = static_cast<int>(sizeof(Shared<D, NT>) + (kCacheMaxSeqs + 1) * 8);
+  // the attribute is the device's: set it once for each (up to 64 devices; every call beyond)
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  const size_t smem = sizeof(Shared<D, NT>) + (static_cast<size_t>(p.st.n_seqs) + 1) * 8;
   cache_attention_kernel<D, NT><<<p.grid, Cfg<D, NT>::NW * 32, smem, stream>>>(p);
   return cudaGetLastError();
 }
-
 }  // namespace
 
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
