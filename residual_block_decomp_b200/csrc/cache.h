@@ -80,11 +80,12 @@ struct CacheAttnParams {
   void* out;
   float* lse;
   uint32_t* cnt;                     // [grid] arrivals of the item that begins in CTA i's range and leaves it
-  float* part;                       // [grid][2] partial results
+  float* part;                       // [grid][2] partial results that other CTAs join
+  float* frag;                       // [grid][warps] partial results that the CTA itself joins
   int grid;
 };
 struct CacheAttnWs {
-  size_t cnt, part, total;
+  size_t cnt, part, frag, total;
 };
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms);
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream);

@@ -195,6 +195,7 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
   p.lse = lse;
   p.cnt = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(workspace) + W.cnt);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.part);
+  p.frag = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.frag);
   p.grid = cache->sm_count;
   return cuda_status(launch_cache_attention(p, cache->dim, static_cast<int>(most), stream));
 }

@@ -44,6 +44,7 @@ namespace bs {
 namespace {
 
 constexpr int kTileBytes5k = 5120;
+constexpr int kWarps = 12;
 constexpr float kNegInf = -INFINITY;
 constexpr float kNothing = -3.0e38f;   // the reference before any score
 constexpr float kLag = 8.0f;           // how far scores may pass it
@@ -58,7 +59,7 @@ struct Cfg {
   static constexpr int OREG = NT * J * 16;                    // accumulators of a lane
   static constexpr int FREG = OREG + 4 * NT;                  // and its maxima and sums
   static constexpr int FBYTES = FREG * 128;                   // a warp's partial result
-  static constexpr int NW = (NT == 1 && D <= 128) ? 12 : 8;   // warps
+  static constexpr int NW = (NT == 1 && D <= 128) ? kWarps : 8;   // warps
   static constexpr int ST = 2;                                // stages of a warp
   static constexpr int UC = chunk_bytes(D) / 16;              // 16-byte units of a chunk
 };
@@ -68,6 +69,8 @@ struct FragMeta {
   long long id;          // number of the item's first tile in the list; -1: no partial result here
   int tiles, seq, h, rt;
 };
+// A warp keeps the partial result of its run's last item in its stages, which are free by then, and that of its
+// first item, if others follow, in the workspace (its own CTA reads it back).
 
 __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
   uint32_t d;
@@ -76,7 +79,7 @@ __device__ __forceinline__ uint32_t movmatrix(uint32_t a) {
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -92,8 +95,15 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
 __device__ __forceinline__ void cp16_zfill(uint32_t dst, const void* src, int n) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
-// (w & 0x00f000f0) | 0x54005400: nibbles 1 and 5 of a word as the fp16 pair 64 + c.
-__device__ __forceinline__ uint32_t pair64(uint32_t w) { return (w & 0x00f000f0u) | 0x54005400u; }
+// (w & mask) | magic in one instruction (both constants in registers).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+// Nibbles 1 and 5 of a word as the fp16 pair 64 + c; nibbles 0 and 4 as 1024 + c.
+__device__ __forceinline__ uint32_t pair64(uint32_t w) { return and_or(w, 0x00f000f0u, 0x54005400u); }
+__device__ __forceinline__ uint32_t pair1024(uint32_t w) { return and_or(w, 0x000f000fu, 0x64006400u); }
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
@@ -130,7 +140,6 @@ template <int D, int NT>
 struct Shared {
   using C = Cfg<D, NT>;
   uint8_t stage[C::NW][C::ST][kTileBytes5k];
-  uint8_t frag[C::NW][C::FBYTES];         // a warp's partial result of its first item; of its last one: in its stages
   FragMeta meta[2 * C::NW];
   int scan[32];
   int last[2];
@@ -525,14 +534,13 @@ struct State {
         const __half2 sy = u2h(__byte_perm(pr[2][j], pr[3][j], 0x5410)), by = u2h(__byte_perm(pr[2][j], pr[3][j], 0x7632));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // nibble e of both halves: 1024 + c in place 0 (0x6400), 64 + c in place 1 (0x5400)
-          const int sh = e & 2 ? 8 : 0;
-          const uint32_t mask = e & 1 ? 0x00f000f0u : 0x000f000fu, magic = e & 1 ? 0x54005400u : 0x64006400u;
-          const __half2 off = e & 1 ? __half2half2(__ushort_as_half(0xd480)) : __half2half2(__ushort_as_half(0xe408));  // -72, -1032
-          const __half2 c0 = __hadd2(u2h(((xl >> sh) & mask) | magic), off);
-          const __half2 c1 = __hadd2(u2h(((xh >> sh) & mask) | magic), off);
-          const __half2 c2 = __hadd2(u2h(((yl >> sh) & mask) | magic), off);
-          const __half2 c3 = __hadd2(u2h(((yh >> sh) & mask) | magic), off);
+          // nibble e of both halves: 1024 + c in place 0, 64 + c in place 1
+          auto code = [&](uint32_t w) {
+            if (e & 2) w >>= 8;
+            return e & 1 ? __hadd2(u2h(pair64(w)), u2h(0xd480d480u))       // - 72
+                         : __hadd2(u2h(pair1024(w)), u2h(0xe408e408u));    // - 1032
+          };
+          const __half2 c0 = code(xl), c1 = code(xh), c2 = code(yl), c3 = code(yh);
           const uint32_t a0 = h2u(__hfma2(c0, sx, bx)), a1 = h2u(__hfma2(c1, sx, bx));
           const uint32_t a2 = h2u(__hfma2(c2, sy, by)), a3 = h2u(__hfma2(c3, sy, by));
 #pragma unroll
@@ -689,7 +697,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     Rows<D, NT> q;
     State<D, NT> st;
     long long item = w0 - c.t;       // number of the item's first tile
-    bool first = true, fresh = true;
+    bool fresh = true;
     int seg0 = c.t;
     int slot = 0;
     while (todo > 0) {
@@ -727,15 +735,11 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
                 write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, st.m[nt][k], st.l[nt][k], lane);
               }
         } else {
-          float* f = reinterpret_cast<float*>(first ? sh.frag[warp] : sh.stage[warp][0]);
-          if (!first) {                      // the run's last item: its stages are free now
-            cp_async_wait<0>();
-            __syncwarp();
-          }
+          float* f = todo > 0 ? p.frag + static_cast<size_t>(blockIdx.x * C::NW + warp) * (C::FREG * 32)
+                              : reinterpret_cast<float*>(sh.stage[warp][0]);
           st.store(f, lane);
-          if (lane == 0) sh.meta[2 * warp + (first ? 0 : 1)] = FragMeta{item, c.tiles, c.seq, c.h, c.rt};
+          if (lane == 0) sh.meta[2 * warp + (todo > 0 ? 0 : 1)] = FragMeta{item, c.tiles, c.seq, c.h, c.rt};
         }
-        first = false;
         if (todo > 0) {
           wk.next_item(c);
           item = w1 - todo;
@@ -751,7 +755,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
   // Join what warps share; of what CTAs share write this CTA's part.
   constexpr int kUnits = NT * C::J * 2;
   auto slot_at = [&](int s) -> const float* {
-    return reinterpret_cast<const float*>(s & 1 ? sh.stage[s >> 1][0] : sh.frag[s >> 1]);
+    return s & 1 ? reinterpret_cast<const float*>(sh.stage[s >> 1][0])
+                 : static_cast<const float*>(p.frag + static_cast<size_t>(blockIdx.x * C::NW + (s >> 1)) * (C::FREG * 32));
   };
   auto cta_of = [&](long long tile) { return static_cast<int>(((tile + 1) * n - 1) / T); };
   int shared_items = 0;
@@ -862,10 +867,12 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   CacheAttnWs w{};
   const int nt = rows > 8 && dim <= 128 ? 2 : 1;
-  const size_t regs = static_cast<size_t>(nt) * (dim / 64) * 16 + 4 * nt;
+  const size_t result = (static_cast<size_t>(nt) * (dim / 64) * 16 + 4 * nt) * 128;
+  const size_t warps = nt == 1 && dim <= 128 ? kWarps : 8;
   w.cnt = 0;
   w.part = (static_cast<size_t>(sms) * 4 + 255) / 256 * 256;
-  w.total = w.part + static_cast<size_t>(sms) * 2 * regs * 128;
+  w.frag = w.part + static_cast<size_t>(sms) * 2 * result;
+  w.total = w.frag + sms * warps * result;
   return w;
 }
 
