@@ -67,7 +67,7 @@ struct Cfg {
 // Partial results are laid out [register][lane].
 struct FragMeta {
   long long id;          // number of the item's first tile in the list; -1: no partial result here
-  int tiles, seq, h, rt;
+  int tiles, row0, rows, h, rt;
 };
 // A warp keeps the partial result of its run's last item in its stages, which are free by then, and that of its
 // first item, if others follow, in the workspace (its own CTA reads it back).
@@ -142,7 +142,7 @@ struct Shared {
   uint8_t stage[C::NW][C::ST][kTileBytes5k];
   FragMeta meta[2 * C::NW];
   int scan[32];
-  int last[2];
+  int last[2];            // slot of a shared item whose parts this CTA adds up; -1: none
   long long scan_total;
   // then long long prefix[n_seqs + 1]
 };
@@ -570,8 +570,8 @@ struct State {
 };
 
 // Writes 8 numbers (dims 8 w ..) of column k of row block nt, and with w == 0 the row's lse.
-template <int D, int NT>
-__device__ __forceinline__ void write_row(const CacheAttnParams& p, const Cursor& c, int nt, int k, int w, const float (&x)[8],
+template <int D, int NT, typename Item>
+__device__ __forceinline__ void write_row(const CacheAttnParams& p, const Item& c, int nt, int k, int w, const float (&x)[8],
                                           float m, float l, int lane) {
   const int row = c.rt * Cfg<D, NT>::R + nt * 8 + (lane & 3) * 2 + k;
   if (row >= c.rows * p.group) return;
@@ -592,28 +592,50 @@ __device__ __forceinline__ void write_row(const CacheAttnParams& p, const Cursor
   if (p.lse != nullptr && w == 0) p.lse[at] = l == 0.0f ? kNegInf : (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// Joins `n` partial results of an item (addresses from `at(i)`, in the order of their tiles) for
-// one block of registers: row block nt, word j, column k (8 numbers of one row per lane).
+// Joins partial results first, first + step, ... < n of an item (addresses from `at(i)`), in that order, for
+// one block of registers: row block nt, word j, column k (8 numbers of one row per lane).  Four are
+// loaded at a time.
 template <int D, int NT, typename At>
-__device__ __forceinline__ void join(int n, const At& at, int nt, int j, int k, int lane, float (&x)[8], float& m,
-                                     float& l) {
+__device__ __forceinline__ void join(int first, int step, int n, const At& at, int nt, int j, int k, int lane, float (&x)[8],
+                                     float& m, float& l) {
   using C = Cfg<D, NT>;
-  const int mr = C::OREG + nt * 4 + k;
+  const int mr = (C::OREG + nt * 4 + k) * 32 + lane, r0 = ((nt * C::J + j) * 16 + k) * 32 + lane;
   m = kNothing;
-  for (int i = 0; i < n; ++i) m = fmaxf(m, at(i)[mr * 32 + lane]);
   l = 0.0f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = 0.0f;
-#pragma unroll 2
-  for (int i = 0; i < n; ++i) {
-    const float* f = at(i);
-    const float wgt = ex2(f[mr * 32 + lane] - m);
-    l = fmaf(wgt, f[(mr + 2) * 32 + lane], l);
+#pragma unroll 1
+  for (int i = first; i < n; i += 4 * step) {
+    float fm[4], fl[4], fx[4][8];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int r = (nt * C::J + j) * 16 + e * 4 + k;
-      x[e] = fmaf(wgt, f[r * 32 + lane], x[e]);               // dim 8 w + e
-      x[4 + e] = fmaf(wgt, f[(r + 2) * 32 + lane], x[4 + e]); // dim 8 w + 4 + e
+    for (int b = 0; b < 4; ++b) {
+      fm[b] = kNothing;
+      fl[b] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) fx[b][e] = 0.0f;
+      if (i + b * step < n) {
+        const float* f = at(i + b * step);
+        fm[b] = f[mr];
+        fl[b] = f[mr + 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          fx[b][e] = f[r0 + e * 128];            // dim 8 w + e
+          fx[b][4 + e] = f[r0 + e * 128 + 64];   // dim 8 w + 4 + e
+        }
+      }
+    }
+    const float top = fmaxf(fmaxf(m, fmaxf(fm[0], fm[1])), fmaxf(fm[2], fm[3]));
+    const float keep = ex2(m - top);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= keep;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float w = ex2(fm[b] - top);
+      l = fmaf(w, fl[b], l);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(w, fx[b][e], x[e]);
     }
   }
 }
@@ -670,7 +692,8 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
       for (size_t e = tid; e < n; e += C::NW * 32) p.lse[at + e] = kNegInf;
   }
 
-  const long long n = T < gridDim.x ? T : gridDim.x;   // CTAs with work
+  // CTAs with work: a tile for every warp before another CTA takes part, as fewer CTAs have less to join
+  const long long n = min(static_cast<long long>(gridDim.x), (T + C::NW - 1) / C::NW);
   if (blockIdx.x >= n) return;
   const long long c0 = T * blockIdx.x / n, c1 = T * (blockIdx.x + 1) / n;
   const long long w0 = c0 + (c1 - c0) * warp / C::NW, w1 = c0 + (c1 - c0) * (warp + 1) / C::NW;
@@ -738,7 +761,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
           float* f = todo > 0 ? p.frag + static_cast<size_t>(blockIdx.x * C::NW + warp) * (C::FREG * 32)
                               : reinterpret_cast<float*>(sh.stage[warp][0]);
           st.store(f, lane);
-          if (lane == 0) sh.meta[2 * warp + (todo > 0 ? 0 : 1)] = FragMeta{item, c.tiles, c.seq, c.h, c.rt};
+          if (lane == 0) sh.meta[2 * warp + (todo > 0 ? 0 : 1)] = FragMeta{item, c.tiles, c.row0, c.rows, c.h, c.rt};
         }
         if (todo > 0) {
           wk.next_item(c);
@@ -752,95 +775,110 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
   }
   __syncthreads();
 
-  // Join what warps share; of what CTAs share write this CTA's part.
+  // Join what warps share; of what CTAs share write this CTA's part.  Slots are in the order of the list, so an
+  // item's are neighbours: every warp finds the items' first slots by vote.
   constexpr int kUnits = NT * C::J * 2;
+  static_assert(2 * C::NW <= 32, "a lane a slot");
+  const long long my_id = lane < 2 * C::NW ? sh.meta[lane].id : -1;
+  const uint32_t present = __ballot_sync(0xffffffffu, my_id >= 0);
+  const uint32_t below = present & ((1u << lane) - 1);
+  const long long prev_id = __shfl_sync(0xffffffffu, my_id, below ? 31 - __clz(below) : lane);
+  const uint32_t heads = __ballot_sync(0xffffffffu, my_id >= 0 && (below == 0 || prev_id != my_id));
   auto slot_at = [&](int s) -> const float* {
     return s & 1 ? reinterpret_cast<const float*>(sh.stage[s >> 1][0])
                  : static_cast<const float*>(p.frag + static_cast<size_t>(blockIdx.x * C::NW + (s >> 1)) * (C::FREG * 32));
   };
   auto cta_of = [&](long long tile) { return static_cast<int>(((tile + 1) * n - 1) / T); };
-  int shared_items = 0;
-  for (int s = 0; s < 2 * C::NW; ++s) {
-    const FragMeta fm = sh.meta[s];
-    if (fm.id < 0) continue;
-    int list[2 * C::NW], cntf = 0, e = s;
-    for (; e < 2 * C::NW; ++e) {
-      if (sh.meta[e].id < 0) continue;
-      if (sh.meta[e].id != fm.id) break;
-      list[cntf++] = e;
-    }
-    const bool whole = fm.id >= c0 && fm.id + fm.tiles <= c1;
-    Cursor c;
-    wk.seq(c, fm.seq);
-    c.h = fm.h;
-    c.rt = fm.rt;
-    const int out_slot = fm.id >= c0 ? 1 : 0;
-    float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + out_slot) * (C::FREG * 32);
-    for (int u = warp; u < kUnits; u += C::NW) {
-      const int k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
-      float x[8], m, l;
-      join<D, NT>(cntf, [&](int i) { return slot_at(list[i]); }, nt, j, k, lane, x, m, l);
-      if (whole) {
-        write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
-      } else {
+  const int n_items = __popc(heads);
+#pragma unroll 1
+  for (int v = warp; v < n_items * kUnits; v += C::NW) {
+    uint32_t hm = heads;
+    for (int i = v / kUnits; i > 0; --i) hm &= hm - 1;
+    const int head = __ffs(hm) - 1;
+    hm &= hm - 1;
+    uint32_t slots = present >> head << head;
+    if (hm != 0) slots &= (hm & -hm) - 1;
+    const FragMeta& fm = sh.meta[head];
+    const int u = v % kUnits, k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
+    float x[8], m, l;
+    join<D, NT>(0, 1, __popc(slots),
+                [&](int) {                     // asked for in order
+                  const int s = __ffs(slots) - 1;
+                  slots &= slots - 1;
+                  return slot_at(s);
+                },
+                nt, j, k, lane, x, m, l);
+    if (fm.id >= c0 && fm.id + fm.tiles <= c1) {
+      write_row<D, NT>(p, fm, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
+    } else {
+      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (fm.id >= c0 ? 1 : 0)) * (C::FREG * 32);
+      const int r0 = ((nt * C::J + j) * 16 + k) * 32 + lane, mr = (C::OREG + nt * 4 + k) * 32 + lane;
 #pragma unroll
-        for (int e2 = 0; e2 < 4; ++e2) {
-          const int r = (nt * C::J + j) * 16 + e2 * 4 + k;
-          part[r * 32 + lane] = x[e2];
-          part[(r + 2) * 32 + lane] = x[4 + e2];
-        }
-        if (j == 0) {
-          part[(C::OREG + nt * 4 + k) * 32 + lane] = m;
-          part[(C::OREG + nt * 4 + 2 + k) * 32 + lane] = l;
+      for (int e = 0; e < 4; ++e) {
+        part[r0 + e * 128] = x[e];
+        part[r0 + e * 128 + 64] = x[4 + e];
+      }
+      if (j == 0) {
+        part[mr] = m;
+        part[mr + 64] = l;
+      }
+    }
+  }
+  if (tid < 2) sh.last[tid] = -1;
+  __syncthreads();
+
+  // Count this CTA's parts (of the item that began before it, and of the one that goes on behind it); the CTA that
+  // counts an item's last one adds them up.  The barrier and the count's release order the parts before it.
+  if (warp == 0) {
+    const bool mine = (heads >> lane) & 1;
+    if (mine) {
+      const FragMeta& fm = sh.meta[lane];
+      if (fm.id < c0 || fm.id + fm.tiles > c1) {
+        const int f0 = cta_of(fm.id), f1 = cta_of(fm.id + fm.tiles - 1);
+        if (atom_add_acq_rel_gpu(p.cnt + f0, 1u) == static_cast<uint32_t>(f1 - f0)) {
+          sh.last[fm.id >= c0 ? 1 : 0] = lane;
+          p.cnt[f0] = 0;          // as the next call needs it; nobody else touches it any more
         }
       }
     }
-    if (!whole) ++shared_items;
-    s = e - 1;
-  }
-  if (shared_items == 0) return;
-
-  // Count this CTA's parts; the CTA that counts an item's last one adds them up.
-  __threadfence();
-  __syncthreads();
-  if (tid < 2) sh.last[tid] = 0;
-  __syncthreads();
-  long long ids[2] = {-1, -1};
-  int which[2] = {0, 0}, items = 0;
-  for (int s = 0; s < 2 * C::NW; ++s) {
-    const long long id = sh.meta[s].id;
-    if (id < 0 || (id >= c0 && id + sh.meta[s].tiles <= c1) || (items > 0 && ids[items - 1] == id)) continue;
-    if (items < 2) {
-      ids[items] = id;
-      which[items++] = s;
-    }
-  }
-  if (tid < items) {
-    const FragMeta fm = sh.meta[which[tid]];
-    const int f0 = cta_of(fm.id), f1 = cta_of(fm.id + fm.tiles - 1);
-    const uint32_t seen = atom_add_acq_rel_gpu(p.cnt + f0, 1u);
-    if (seen == static_cast<uint32_t>(f1 - f0)) {
-      sh.last[tid] = 1;
-      p.cnt[f0] = 0;          // as the next call needs it; nobody else touches it any more
-    }
   }
   __syncthreads();
-  for (int it = 0; it < items; ++it) {
-    if (!sh.last[it]) continue;
-    const FragMeta fm = sh.meta[which[it]];
-    const int f0 = cta_of(fm.id), f1 = cta_of(fm.id + fm.tiles - 1);
-    Cursor c;
-    wk.seq(c, fm.seq);
-    c.h = fm.h;
-    c.rt = fm.rt;
-    for (int u = warp; u < kUnits; u += C::NW) {
-      const int k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
-      float x[8], m, l;
-      join<D, NT>(f1 - f0 + 1,
-                  [&](int i) { return static_cast<const float*>(p.part + static_cast<size_t>((f0 + i) * 2 + (i == 0 ? 1 : 0)) * (C::FREG * 32)); },
+  constexpr int kGroups = C::NW / kUnits;      // warps of a block of registers share the parts
+  float* scratch = reinterpret_cast<float*>(sh.stage);
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it) {
+    const int slot = sh.last[it];
+    if (slot < 0) continue;
+    const FragMeta& fm = sh.meta[slot];
+    const int f0 = cta_of(fm.id), parts = cta_of(fm.id + fm.tiles - 1) - f0 + 1;
+    const int u = warp % kUnits, grp = warp / kUnits, k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
+    const float* base = p.part + static_cast<size_t>(f0) * 2 * (C::FREG * 32);
+    float x[8], m, l;
+    if (grp < kGroups)
+      join<D, NT>(grp, kGroups, parts, [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? 1 : 0)) * (C::FREG * 32); },
                   nt, j, k, lane, x, m, l);
-      write_row<D, NT>(p, c, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
+    if (kGroups > 1) {
+      float* mine = scratch + (it * C::NW + warp) * 320 + lane;
+      if (grp > 0 && grp < kGroups) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mine[e * 32] = x[e];
+        mine[256] = m;
+        mine[288] = l;
+      }
+      __syncthreads();
+      if (grp == 0) {
+#pragma unroll 1
+        for (int g = 1; g < kGroups; ++g) {
+          const float* f = scratch + (it * C::NW + g * kUnits + u) * 320 + lane;
+          const float top = fmaxf(m, f[256]), keep = ex2(m - top), w = ex2(f[256] - top);
+          m = top;
+          l = l * keep + w * f[288];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = x[e] * keep + w * f[e * 32];
+        }
+      }
     }
+    if (grp == 0) write_row<D, NT>(p, fm, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
   }
 }
 
