@@ -21,12 +21,16 @@ _BINDING_NAMES = (
     "CacheStep", "bs_cache_append", "bs_cache_attention", "bs_cache_attention_workspace_bytes", "bs_cache_create",
     "bs_cache_destroy", "bs_cache_device_bytes", "bs_cache_get_device_error", "bs_cache_page_bytes", "bs_cache_read",
 )
-__all__ = list(_BINDING_NAMES) + ["BitStackLinear"]
+_LAYER_NAMES = ("BitStackLinear",)
+__all__ = list(_BINDING_NAMES) + list(_LAYER_NAMES)
 
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
-    if name == "BitStackLinear":
-        return importlib.import_module(".layer", __name__).BitStackLinear
-    raise AttributeError(name)
+        value = getattr(importlib.import_module(".binding", __name__), name)
+    elif name in _LAYER_NAMES:
+        value = getattr(importlib.import_module(".layer", __name__), name)
+    else:
+        raise AttributeError(name)
+    globals()[name] = value   # found directly from now on
+    return value

@@ -122,8 +122,9 @@ def _stream(stream) -> int | None:
     """A cudaStream_t as an int: a torch stream, a raw handle, or None (current stream)."""
     if stream is None:
         import torch
-        if torch.cuda.is_available():
-            return torch.cuda.current_stream().cuda_stream or None
+        if torch.cuda.is_initialized() or torch.cuda.is_available():
+            # the handle of torch.cuda.current_stream(), without building a Stream object
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
         return None
     if hasattr(stream, "cuda_stream"):
         return stream.cuda_stream or None
@@ -138,9 +139,14 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float16: BS_F16, torch.bfloat16: BS_BF16, torch.float32: BS_F32}[t.dtype]
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float16: BS_F16, torch.bfloat16: BS_BF16, torch.float32: BS_F32})
+    return _dtype_codes[t.dtype]
 
 
 # ------------------------------------------------------------------ sizes ----------

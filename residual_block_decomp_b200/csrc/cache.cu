@@ -186,47 +186,87 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
   }
 }
 
-// grid as above.  Rows of an empty slot, and of pages outside the pool, are zeros.
-template <int D, typename T, int U>
+// 8 codes of a word as numbers b + s (c - 8).
+__device__ __forceinline__ void numbers(uint32_t w, uint32_t pair, float (&x)[8]) {
+  const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pair));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    // nibbles k and k + 4: 64 + c (k odd) or 1024 + c in fp16, exact
+    uint32_t v = k & 2 ? w >> 8 : w;
+    v = k & 1 ? (v & 0x00f000f0u) | 0x54005400u : (v & 0x000f000fu) | 0x64006400u;
+    const uint32_t off = k & 1 ? 0xd480d480u : 0xe408e408u;   // - 72, - 1032
+    const float2 c = __half22float2(__hadd2(*reinterpret_cast<const __half2*>(&v), *reinterpret_cast<const __half2*>(&off)));
+    x[k] = fmaf(sb.x, c.x, sb.y);
+    x[k + 4] = fmaf(sb.x, c.y, sb.y);
+  }
+}
+
+// A warp reads one chunk of one head: 16 bytes of codes a lane and access, a quarter to a whole row's worth of
+// consecutive lanes, with the pairs they need; a store writes 8 numbers.  grid: (blocks of chunks and heads of a
+// sequence, sequences).  Rows of an empty slot, and of pages outside the pool, are zeros.
+template <int D, typename T>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ CacheCopyParams p) {
-  const int seq = blockIdx.y;
+  constexpr int UR = D / 32;                     // 16-byte units of a row of codes
+  constexpr int N = 16 * UR / 32;                // units of a lane: keys, and as many of values
+  constexpr int GR = D / 32, J = D / 64;
+  const int seq = blockIdx.y, lane = threadIdx.x & 31;
   const SeqSpan s = seq_span(p.st, seq);
   if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
-  const unsigned units = static_cast<unsigned>(s.rows) * p.st.heads * 2 * (D / 8);
-  for (unsigned base = blockIdx.x * (kThreads * U); base < units; base += gridDim.x * (kThreads * U)) {
-    uint32_t word[U], pair[U];
-    T* to[U];
+  if (s.rows == 0) return;
+  const int heads = p.st.heads;
+  const int start = s.live ? s.start : 0;        // an empty slot's rows go by as if they stood at 0
+  const int first = start / kChunkTokens;
+  const unsigned chunks = static_cast<unsigned>((start + s.rows - 1) / kChunkTokens - first + 1);
+  const unsigned warps = gridDim.x * (kThreads / 32);
+  for (unsigned v = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); v < chunks * heads; v += warps) {
+    const int h = static_cast<int>(v % heads), pos0 = (first + static_cast<int>(v / heads)) * kChunkTokens;
+    const uint8_t* ch = nullptr;
+    if (s.live) {
+      const int page = __ldg(p.st.table + static_cast<size_t>(seq) * p.st.stride + (pos0 >> p.st.page_shift));
+      ch = chunk_at(p.st, page, pos0, h, D);
+      if (ch == nullptr && lane == 0) atomicOr(p.st.err, kErrRange);
+    }
+    uint4 code[2][N], pair[2][N];
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const unsigned u = base + e * kThreads + threadIdx.x;
-      word[e] = pair[e] = 0;
-      to[e] = nullptr;
-      if (u < units) {
-        const Unit<D> un(u, p.st.heads);
-        T* out = static_cast<T*>(p.out[un.value ? 1 : 0]);
-        if (out == nullptr) continue;
-        to[e] = out + (static_cast<size_t>(s.row0 + un.i) * p.st.heads + un.h) * D + un.w * 8;
-        if (!s.live) continue;
-        uint32_t* pp;
-        const uint32_t* wp = unit_bytes<D>(p.st, seq, s.start, un, &pp);
-        if (wp == nullptr) {
-          atomicOr(p.st.err, kErrRange);
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int u = i * 32 + lane, row = u / UR, c = u % UR;
+        const int r = pos0 + (kv ? (row & 7) * 2 + (row >> 3) : row) - start;
+        code[kv][i] = pair[kv][i] = make_uint4(0, 0, 0, 0);
+        if (ch == nullptr || r < 0 || r >= s.rows || p.out[kv] == nullptr) continue;
+        const uint8_t* base = ch + kv * 10 * D;
+        code[kv][i] = __ldg(reinterpret_cast<const uint4*>(base + u * 16));
+        const uint8_t* pr = base + 8 * D + row * (D / 8);
+        if (kv ? J == 4 : GR >= 4) {             // four consecutive pairs
+          pair[kv][i] = __ldg(reinterpret_cast<const uint4*>(pr + (kv ? c / 4 : c % (GR / 4)) * 16));
+        } else if (kv ? J == 2 : true) {         // two, for words 0, 1 and 2, 3
+          const uint2 two = __ldg(reinterpret_cast<const uint2*>(pr + (kv ? c / 2 * 8 : 0)));
+          pair[kv][i] = make_uint4(two.x, two.y, two.x, two.y);
         } else {
-          word[e] = *wp;
-          pair[e] = *pp;
+          const uint32_t one = __ldg(reinterpret_cast<const uint32_t*>(pr + c * 4));
+          pair[kv][i] = make_uint4(one, one, one, one);
         }
       }
-    }
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      if (to[e] == nullptr) continue;
-      const float2 sb = __half22float2(*reinterpret_cast<const __half2*>(&pair[e]));
-      float x[8];
+    for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        x[k] = fmaf(sb.x, static_cast<float>((word[e] >> (4 * k)) & 15u) - 8.0f, sb.y);
-      Eight<T>::store(to[e], x);
-    }
+      for (int i = 0; i < N; ++i) {
+        const int u = i * 32 + lane, row = u / UR, c = u % UR;
+        const int r = pos0 + (kv ? (row & 7) * 2 + (row >> 3) : row) - start;
+        if (r < 0 || r >= s.rows || p.out[kv] == nullptr) continue;
+        T* out = static_cast<T*>(p.out[kv]) + (static_cast<size_t>(s.row0 + r) * heads + h) * D;
+        const uint32_t cw[4] = {code[kv][i].x, code[kv][i].y, code[kv][i].z, code[kv][i].w};
+        const uint32_t pw[4] = {pair[kv][i].x, pair[kv][i].y, pair[kv][i].z, pair[kv][i].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int place = 4 * c + e;
+          const int w = kv ? place / J + 8 * (place % J) : 4 * (place % GR) + place / GR;
+          float x[8];
+          numbers(cw[e], pw[e], x);
+          Eight<T>::store(out + w * 8, x);
+        }
+      }
   }
 }
 
@@ -250,11 +290,11 @@ cudaError_t append_as(const CacheCopyParams& p, cudaStream_t stream) {
 }
 template <int D, typename T>
 cudaError_t read_as(const CacheCopyParams& p, cudaStream_t stream) {
-  const long long units = static_cast<long long>(p.st.n_tokens) * p.st.heads * 2 * (D / 8);
-  if (units >= 148ll * 8 * kThreads * 4)
-    cache_read_kernel<D, T, 4><<<copy_grid<D, 4>(p.st), kThreads, 0, stream>>>(p);
-  else
-    cache_read_kernel<D, T, 1><<<copy_grid<D, 1>(p.st), kThreads, 0, stream>>>(p);
+  // a sequence of n positions touches at most n / 16 + 2 chunks
+  const long long longest = p.st.max_new < p.st.n_tokens ? p.st.max_new : p.st.n_tokens;
+  const long long blocks = ((longest / kChunkTokens + 2) * p.st.heads + kThreads / 32 - 1) / (kThreads / 32);
+  const dim3 grid(static_cast<unsigned>(blocks > 65535 ? 65535 : blocks), static_cast<unsigned>(p.st.n_seqs));
+  cache_read_kernel<D, T><<<grid, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 template <int D>
