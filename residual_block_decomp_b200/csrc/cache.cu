@@ -2,14 +2,13 @@
 // back.  The layout of a page and the arithmetic of a group are stated in
 // include/bitstack.h.
 //
-// Both kernels work in units of one code word, 8 consecutive numbers of one (token,
-// head, keys or values): a thread moves 16 bytes of dense numbers (32 for fp32), four
-// neighbouring lanes hold a group of 32, and a warp covers whole rows, so dense accesses
-// are contiguous and packed ones stay within a row's 32 to 128 bytes.
+// A thread takes 8 dense numbers at a time (16 bytes, 32 for fp32) or 16 bytes of codes; dense accesses are
+// contiguous over a row's lanes and packed ones stay within its 32 to 128 bytes.
 //
 // A group is s = fp16((max - min) / 15), b = fp16(min + 8 (max - min) / 15),
-// c = rint((x - b) / s + 8).  The quotient is a true division and the statistics are
-// taken in fp32, so the codes are those of the definition for every input.
+// c = rint((x - b) / s + 8) in fp32.  A true division for every number made the writing kernel
+// compute bound (25 instructions a number); the reciprocal decides all codes but those
+// next to a rounding border, which are divided, so the codes are the definition's for every input.
 //
 // Both are bound by memory traffic: 4 bytes dense and 1.25 packed a number pair.
 #include <cuda_bf16.h>
@@ -35,40 +34,17 @@ __device__ __forceinline__ int pair_place(bool value, int g) {
 }
 __device__ __forceinline__ int token_row(bool value, int t) { return value ? (t >> 1) + 8 * (t & 1) : t; }
 
-// One unit of a sequence: word w of token i, head h, keys (value false) or values.
-template <int D>
-struct Unit {
-  int w, h, i;
-  bool value;
-  __device__ Unit(unsigned u, int heads) {
-    w = u % (D / 8);
-    u /= D / 8;
-    value = u & 1;
-    u >>= 1;
-    i = static_cast<int>(u / static_cast<unsigned>(heads));
-    h = static_cast<int>(u % static_cast<unsigned>(heads));
-  }
-};
-
-// Address of a unit's code word; its pair is at the returned `pair`.
-template <int D>
-__device__ __forceinline__ uint32_t* unit_bytes(const StepParams& p, int seq, int start, const Unit<D>& u,
-                                                uint32_t** pair) {
-  const int pos = start + u.i;
-  const int page = p.table[static_cast<size_t>(seq) * p.stride + (pos >> p.page_shift)];
-  uint8_t* c = chunk_at(p, page, pos, u.h, D);
-  if (c == nullptr) return nullptr;
-  if (u.value) c += 10 * D;
-  const int row = token_row(u.value, pos & (kChunkTokens - 1));
-  *pair = reinterpret_cast<uint32_t*>(c + 8 * D + row * (D / 8)) + pair_place<D>(u.value, u.w >> 2);
-  return reinterpret_cast<uint32_t*>(c + row * (D / 2)) + word_place<D>(u.value, u.w);
-}
-
 template <typename T>
 struct Eight;   // 8 dense numbers
+// Whether some 16-bit number of two packed ones, signs aside, is at or above `least`.
+__device__ __forceinline__ bool reaches(uint4 a, uint32_t least) {
+  const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
+  return (m & 0xffffu) >= least || (m >> 16) >= least;
+}
 template <>
 struct Eight<__half> {
   uint4 a;
+  __device__ bool beyond() const { return reaches(a, 0x7bf0u); }   // the first fp16 number above 65000, inf, NaN
   __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
@@ -92,6 +68,7 @@ struct Eight<__half> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
+  __device__ bool beyond() const { return reaches(a, 0x477eu); }   // the first bf16 number above 65000, inf, NaN
   __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
@@ -114,6 +91,12 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<float> {
   float4 a, b;
+  __device__ bool beyond() const {
+    const float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
+                          fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
+    const float sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));   // NaN if one is
+    return m > kCacheClamp || sum != sum;
+  }
   __device__ void load(const void* p) {
     a = __ldg(static_cast<const float4*>(p));
     b = __ldg(static_cast<const float4*>(p) + 1);
@@ -128,59 +111,94 @@ struct Eight<float> {
   }
 };
 
-// grid: (blocks of units of a sequence, sequences); U units a thread, all loads first.
-template <int D, typename T, int U>
+// A warp quantises the keys and values of one token for HB heads, 8 numbers a lane and step, all loads first.
+// The token's page is looked up once.  grid: (blocks of tokens and head blocks of a sequence, sequences).
+template <int D, typename T, int STEPS>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ CacheCopyParams p) {
-  const int seq = blockIdx.y;
+  constexpr int LR = D / 8;                      // lanes of a row
+  constexpr int HB = STEPS * 16 / LR;            // heads of a warp's step run
+  const int seq = blockIdx.y, lane = threadIdx.x & 31;
   const SeqSpan s = seq_span(p.st, seq);
   if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
   if (!s.live) return;
-  const unsigned units = static_cast<unsigned>(s.rows) * p.st.heads * 2 * (D / 8);
-  for (unsigned base = blockIdx.x * (kThreads * U); base < units; base += gridDim.x * (kThreads * U)) {
-    Eight<T> in[U];
-    uint32_t *word[U], *pair[U];
+  const int heads = p.st.heads;
+  const unsigned blocks = (heads + HB - 1) / HB, jobs = static_cast<unsigned>(s.rows) * blocks;
+  const unsigned warps = gridDim.x * (kThreads / 32);
+  for (unsigned v = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); v < jobs; v += warps) {
+    const int i = static_cast<int>(v / blocks), h0 = static_cast<int>(v % blocks) * HB;
+    const int pos = s.start + i;
+    Eight<T> in[STEPS];
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
-      const unsigned u = base + e * kThreads + threadIdx.x;
-      word[e] = nullptr;
+    for (int e = 0; e < STEPS; ++e) {
+      const int u = e * 32 + lane, h = h0 + u / (2 * LR), kv = u / LR % 2;
       in[e] = Eight<T>{};
-      if (u < units) {
-        const Unit<D> un(u, p.st.heads);
-        const int kv = un.value ? 1 : 0;
-        in[e].load(static_cast<const T*>(p.in[kv]) + (s.row0 + un.i) * p.tok[kv] + un.h * p.head[kv] + un.w * 8);
-        word[e] = unit_bytes<D>(p.st, seq, s.start, un, &pair[e]);
-        if (word[e] == nullptr) atomicOr(p.st.err, kErrRange);
-      }
+      if (h < heads)
+        in[e].load(static_cast<const T*>(p.in[kv]) + (s.row0 + i) * p.tok[kv] + h * p.head[kv] + u % LR * 8);
     }
+    const int page = __ldg(p.st.table + static_cast<size_t>(seq) * p.st.stride + (pos >> p.st.page_shift));
+    uint8_t* ch = chunk_at(p.st, page, pos, h0, D);
+    if (ch == nullptr) {
+      if (lane == 0) atomicOr(p.st.err, kErrRange);
+      continue;
+    }
+    const int head_bytes = (1 << p.st.page_shift) / kChunkTokens * chunk_bytes(D);
 #pragma unroll
-    for (int e = 0; e < U; ++e) {
+    for (int e = 0; e < STEPS; ++e) {
+      const int u = e * 32 + lane, hd = u / (2 * LR), kv = u / LR % 2, word = u % LR;
       float x[8];
       in[e].get(x);
-      float lo = kCacheClamp, hi = -kCacheClamp;
+      if (in[e].beyond()) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        x[k] = x[k] != x[k] ? 0.0f : fminf(fmaxf(x[k], -kCacheClamp), kCacheClamp);
-        lo = fminf(lo, x[k]);
-        hi = fmaxf(hi, x[k]);
+        for (int k = 0; k < 8; ++k) x[k] = x[k] != x[k] ? 0.0f : fminf(fmaxf(x[k], -kCacheClamp), kCacheClamp);
       }
+      float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+      float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
-      for (int o = 1; o < 4; o *= 2) {
+      for (int o = 1; o < 4; o *= 2) {           // a group is four lanes
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
         hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
       }
       const float step = __fdiv_rn(hi - lo, 15.0f);
       const __half sh = __float2half_rn(step), bh = __float2half_rn(fmaf(8.0f, step, lo));
       const float sf = __half2float(sh), bf = __half2float(bh);
+      // c = rint((x - b) / s + 8), by the reciprocal where that decides it: the quotient is at most 24 in size
+      // (8 + the rounding of s and b, or clamped beyond), so y is within 2^-16 of it, and so is the sum
+      const float inv = __frcp_rn(sf);
+      constexpr float kInt = 12582912.0f;        // 1.5 2^23: adding it rounds to an integer
       uint32_t w = 0;
+      float far[8], most = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float c = sf > 0.0f ? rintf(__fadd_rn(__fdiv_rn(x[k] - bf, sf), 8.0f)) : 8.0f;
-        w |= static_cast<uint32_t>(fminf(fmaxf(c, 0.0f), 15.0f)) << (4 * k);
+        const float y = fminf(fmaxf(fmaf(x[k] - bf, inv, 8.0f), 0.0f), 15.0f);
+        const float r = y + kInt;
+        far[k] = fabsf(y - (r - kInt));
+        most = fmaxf(most, far[k]);
+        w |= (__float_as_uint(r) & 15u) << (4 * k);
       }
-      if (word[e] != nullptr) {
-        *word[e] = w;
-        if ((threadIdx.x & 3) == 0)
-          *pair[e] = static_cast<uint32_t>(__half_as_ushort(sh)) | static_cast<uint32_t>(__half_as_ushort(bh)) << 16;
+      constexpr float kBorder = 0.5f - 0x1p-16f;
+      if (!(sf > 0.0f)) {
+        w = 0x88888888u;
+      } else if (most > kBorder) {               // next to a half (numbers on a coarse grid often are): divide
+        uint32_t which = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) which |= far[k] > kBorder ? 1u << k : 0u;
+#pragma unroll 1
+        for (; which != 0; which &= which - 1) {
+          const int k = __ffs(which) - 1;
+          float xk = x[0];
+#pragma unroll
+          for (int q = 1; q < 8; ++q) xk = k == q ? x[q] : xk;
+          const float c = fminf(fmaxf(rintf(__fadd_rn(__fdiv_rn(xk - bf, sf), 8.0f)), 0.0f), 15.0f);
+          w = (w & ~(15u << (4 * k))) | static_cast<uint32_t>(c) << (4 * k);
+        }
+      }
+      if (h0 + hd < heads) {
+        uint8_t* at = ch + hd * head_bytes + kv * 10 * D;
+        const int row = token_row(kv != 0, pos & (kChunkTokens - 1));
+        reinterpret_cast<uint32_t*>(at + row * (D / 2))[word_place<D>(kv != 0, word)] = w;
+        if ((lane & 3) == 0)
+          reinterpret_cast<uint32_t*>(at + 8 * D + row * (D / 8))[pair_place<D>(kv != 0, word >> 2)] =
+              static_cast<uint32_t>(__half_as_ushort(sh)) | static_cast<uint32_t>(__half_as_ushort(bh)) << 16;
       }
     }
   }
@@ -271,30 +289,28 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 }
 
 // Blocks for the longest sequence the step may hold; sequences loop over theirs.
-template <int D, int U>
-dim3 copy_grid(const StepParams& s) {
-  const long long longest = s.max_new < s.n_tokens ? s.max_new : s.n_tokens;
-  const long long units = longest * s.heads * 2 * (D / 8);
-  const long long blocks = (units + kThreads * U - 1) / (kThreads * U);
+dim3 copy_grid(const StepParams& s, long long warps_of_longest) {
+  const long long blocks = (warps_of_longest + kThreads / 32 - 1) / (kThreads / 32);
   return dim3(static_cast<unsigned>(blocks < 1 ? 1 : (blocks > 65535 ? 65535 : blocks)), static_cast<unsigned>(s.n_seqs));
 }
+long long longest(const StepParams& s) { return s.max_new < s.n_tokens ? s.max_new : s.n_tokens; }
 
+template <int D, typename T, int STEPS>
+cudaError_t append_steps(const CacheCopyParams& p, cudaStream_t stream) {
+  constexpr int HB = STEPS * 16 / (D / 8);
+  cache_append_kernel<D, T, STEPS><<<copy_grid(p.st, longest(p.st) * ((p.st.heads + HB - 1) / HB)), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+// Four steps of loads in flight a lane where there is work for all SMs' warps, the fewest otherwise.
 template <int D, typename T>
 cudaError_t append_as(const CacheCopyParams& p, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.st.n_tokens) * p.st.heads * 2 * (D / 8);
-  if (units >= 148ll * 8 * kThreads * 4)
-    cache_append_kernel<D, T, 4><<<copy_grid<D, 4>(p.st), kThreads, 0, stream>>>(p);
-  else
-    cache_append_kernel<D, T, 1><<<copy_grid<D, 1>(p.st), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return units >= 148ll * 64 * 32 * 4 ? append_steps<D, T, 4>(p, stream) : append_steps<D, T, D == 256 ? 2 : 1>(p, stream);
 }
 template <int D, typename T>
 cudaError_t read_as(const CacheCopyParams& p, cudaStream_t stream) {
   // a sequence of n positions touches at most n / 16 + 2 chunks
-  const long long longest = p.st.max_new < p.st.n_tokens ? p.st.max_new : p.st.n_tokens;
-  const long long blocks = ((longest / kChunkTokens + 2) * p.st.heads + kThreads / 32 - 1) / (kThreads / 32);
-  const dim3 grid(static_cast<unsigned>(blocks > 65535 ? 65535 : blocks), static_cast<unsigned>(p.st.n_seqs));
-  cache_read_kernel<D, T><<<grid, kThreads, 0, stream>>>(p);
+  cache_read_kernel<D, T><<<copy_grid(p.st, (longest(p.st) / kChunkTokens + 2) * p.st.heads), kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 template <int D>
