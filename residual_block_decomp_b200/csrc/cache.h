@@ -6,12 +6,13 @@
 #include <cstddef>
 #include <cstdint>
 
-#include "../../include/bitstack.h"
+#include "internal.h"
 
 namespace bs {
 
 constexpr int kChunkTokens = 16;     // tokens of a chunk: one matrix tile's rows
 constexpr int kCacheMaxSeqs = 4096;  // sequences of a step (their tile counts are prefix-summed in shared memory)
+
 constexpr uint32_t kErrRange = 2u;   // device error word bit: a step left its bounds
 
 __host__ __device__ constexpr int chunk_bytes(int dim) { return 20 * dim; }
@@ -83,12 +84,18 @@ struct CacheAttnParams {
   float* part;                       // [grid][2] partial results that other CTAs join
   float* frag;                       // [grid][warps] partial results that the CTA itself joins
   int grid;
+  unsigned long long timeout_ns;     // bound on every wait of the kernel for many rows
 };
 struct CacheAttnWs {
   size_t cnt, part, frag, total;
 };
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms);
+bool cache_attn_many(int dim, int rows, int n_seqs);   // whether `rows` query rows a head run on the kernel for many
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream);
+// The kernel for many rows (cache_prefill.cu).
+size_t cache_prefill_smem(int dim, int n_seqs);
+size_t cache_prefill_part_floats(int dim);             // of one partial result
+cudaError_t launch_cache_prefill(const CacheAttnParams& p, int dim, cudaStream_t stream);
 
 struct CacheCopyParams {
   StepParams st;

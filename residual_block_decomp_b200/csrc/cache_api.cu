@@ -197,6 +197,7 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.part);
   p.frag = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.frag);
   p.grid = cache->sm_count;
+  p.timeout_ns = 500000000ull;
   return cuda_status(launch_cache_attention(p, cache->dim, static_cast<int>(most), stream));
 }
 
@@ -206,7 +207,7 @@ bs_status bs_cache_get_device_error(bs_cache_t cache) {
   if (cudaMemcpy(&v, cache->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return BS_ERR_CUDA;
   if (v == 0) return BS_OK;
   if (cudaMemset(cache->err, 0, sizeof(v)) != cudaSuccess) return BS_ERR_CUDA;
-  return (v & kErrRange) ? BS_ERR_RANGE : BS_ERR_CUDA;
+  return (v & kErrTimeout) ? BS_ERR_TIMEOUT : (v & kErrRange) ? BS_ERR_RANGE : BS_ERR_CUDA;
 }
 
 }  // extern "C"

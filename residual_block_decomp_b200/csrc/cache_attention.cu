@@ -902,6 +902,9 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
 }
 }  // namespace
 
+// Rows of a head from which the kernel for many rows is the faster one.
+bool cache_attn_many(int dim, int rows, int n_seqs) { return rows > 32 && cache_prefill_smem(dim, n_seqs) <= 227 * 1024; }
+
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   CacheAttnWs w{};
   const int nt = rows > 8 && dim <= 128 ? 2 : 1;
@@ -911,12 +914,18 @@ CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   w.part = (static_cast<size_t>(sms) * 4 + 255) / 256 * 256;
   w.frag = w.part + static_cast<size_t>(sms) * 2 * result;
   w.total = w.frag + sms * warps * result;
+  // the kernel for many rows has larger parts and no others
+  if (cache_attn_many(dim, rows, 1)) {
+    const size_t many = w.part + static_cast<size_t>(sms) * 2 * cache_prefill_part_floats(dim) * 4;
+    if (many > w.total) w.total = many;
+  }
   return w;
 }
 
 // Rows of an item: 8, or 16 where a head has more than 8 (the packed bytes are then
 // unpacked half as often); D = 256 keeps 8, whose accumulators are 64 registers already.
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream) {
+  if (cache_attn_many(dim, rows, p.st.n_seqs)) return launch_cache_prefill(p, dim, stream);
   if (dim == 64) return rows > 8 ? launch_as<64, 2>(p, stream) : launch_as<64, 1>(p, stream);
   if (dim == 128) return rows > 8 ? launch_as<128, 2>(p, stream) : launch_as<128, 1>(p, stream);
   return launch_as<256, 1>(p, stream);

@@ -1,0 +1,777 @@
+// Attention over the packed key/value cache for many query rows per key/value head: a prompt's pieces, or many
+// drafted tokens (include/bitstack.h, bs_cache_attention; few rows: cache_attention.cu, whose comments state the
+// list of tiles and how it is split).
+//
+// With hundreds of query rows the products bound the time, so they run on tcgen05: an item is one (sequence, head,
+// tile of up to 256 query rows), its context is taken in tiles of 64 tokens, and a tile's packed bytes are expanded
+// once in shared memory for all rows.  Per tile and group of 128 rows
+//     S = Q K^T   (M = 128, N = 64, shared memory operands, fp32 in tensor memory)
+//     P = 2^(S f - m) as fp16, written over S in tensor memory
+//     O += P V    (A from tensor memory, B = V with the dims contiguous)
+// with the maximum and sum of a row in the registers of the thread that owns it.  As in the kernel for few rows the
+// reference m follows the maximum only when a score passes it by 2^8, so O is hardly ever rescaled.
+//
+// Scores stay exact to fp32: a key is b + s (c - 8); s (c - 8) / 2 has 15 bits, so fp16 parts hi = round(s (c - 8) / 2)
+// and lo = the fma's remainder hold it exactly (halved, as s (c - 8) alone may pass fp16's range), and the b of a group
+// meets the sum of its query numbers in 16 more columns (b in fp16 as stored, the sums in two fp16 parts).  So S costs
+// 17 products of K = 16 instead of 8 (D = 128): one fp16 rounding of the keys would have moved the weights by as much
+// as the rounding of P does, and the lse, which is fp32, by more than fp32 allows.  Values are rounded to fp16 by
+// one fma.
+//
+// Roles: 4 warps a group own its rows (softmax, output); 4 warps copy packed tiles ahead and expand them
+// (K and V stages); one thread issues all products: S of tile t before O of tile t - 1, so the tensor pipe has
+// work while the rows' threads are at tile t.
+//
+// 8 numbers of a word are kept in the order (0, 4, 1, 5, 2, 6, 3, 7) that unpacking gives, in Q and K alike (a sum
+// does not mind), and in V as the order of O's columns, undone where rows are written.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <atomic>
+
+#include "cache.h"
+#include "ptx.cuh"
+
+namespace bs {
+namespace {
+
+constexpr int BT = 64;                  // tokens of a tile
+constexpr float kNothing = -3.0e38f;    // the reference before any score
+constexpr float kLag = 8.0f;            // how far scores may pass it
+
+template <int D>
+struct PCfg {
+  static constexpr int G = D == 256 ? 1 : 2;               // groups of 128 rows (tensor memory: 128 + D columns each)
+  static constexpr int R = 128 * G;
+  static constexpr int ST = D == 256 ? 1 : 2;              // K and V stages
+  static constexpr int AHEAD = D == 256 ? 1 : 2;           // packed tiles requested ahead of the one in use
+  static constexpr int H = D / 64;                         // 128-byte columns blocks of a row
+  static constexpr int GR = D / 32;
+  static constexpr int TILE_BYTES = BT / kChunkTokens * chunk_bytes(D);
+  static constexpr int THREADS = G * 128 + 128 + 32;
+  static constexpr int O_COL = G * 128;                    // tensor memory columns: S of group g, buffer b at 128 g + 64 b
+  static constexpr uint32_t TMEM = 512;
+};
+
+template <int D>
+struct alignas(1024) PShared {
+  using C = PCfg<D>;
+  uint8_t q[C::G][C::H][128 * 128];     // 128-byte swizzled rows
+  uint8_t khi[C::ST][C::H][BT * 128];
+  uint8_t klo[C::ST][C::H][BT * 128];
+  uint8_t v[C::ST][C::H][BT * 128];
+  uint8_t qx[C::G][128 * 32];           // the 16 columns of sums and of b: core matrices of 8 rows x 16 bytes
+  uint8_t kx[C::ST][BT * 32];
+  uint8_t staging[C::AHEAD + 1][C::TILE_BYTES];
+  uint64_t kfull[C::ST], kempty[C::ST], vfull[C::ST], vempty[C::ST];
+  uint64_t qfull[C::G], sfull[C::G][2], pfull[C::G][2], pvdone[C::G][2], drained;
+  long long scan_total, wsum[16];
+  uint32_t tmem;
+  int abort, last[2];
+  int good[4];                          // chunks of tile i % 4 that are in the pool
+  // then long long prefix[n_seqs + 1]
+};
+
+// A run of tiles of one item: tiles t0 .. t1 - 1 of `tiles`.
+struct Segment {
+  long long id;                         // number of the item's first tile
+  int seq, row0, rows, start;           // the sequence
+  int rt, h, first, tiles;              // the item: its row tile, head, first position and tiles
+  int t0, t1;
+  int end;                              // positions its last row sees
+};
+
+template <int D>
+struct List {
+  using C = PCfg<D>;
+  const CacheAttnParams& p;
+  const long long* prefix;
+
+  // First position, positions seen and tiles of row tile rt of a sequence.
+  __device__ void item(const SeqSpan& s, int rt, int& first, int& end, int& tiles) const {
+    const int total = s.rows * p.group;
+    const int lowest = s.start + rt * C::R / p.group;
+    end = s.start + (min((rt + 1) * C::R, total) - 1) / p.group + 1;
+    first = lowest >= p.window ? (lowest - p.window + 1) / kChunkTokens * kChunkTokens : 0;
+    tiles = (end - first + BT - 1) / BT;
+  }
+  __device__ long long count(int i) const {
+    const SeqSpan s = seq_span(p.st, i);
+    if (!s.live) return 0;
+    const int rts = (s.rows * p.group + C::R - 1) / C::R;
+    long long n = 0;
+    for (int rt = 0; rt < rts; ++rt) {
+      int first, end, tiles;
+      item(s, rt, first, end, tiles);
+      n += tiles;
+    }
+    return n * p.st.heads;
+  }
+  // The segment that begins at `tile` and goes no further than `stop`.
+  __device__ Segment at(long long tile, long long stop) const {
+    int lo = 0, hi = p.st.n_seqs - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) / 2;
+      if (prefix[mid] <= tile) lo = mid;
+      else hi = mid - 1;
+    }
+    const SeqSpan s = seq_span(p.st, lo);
+    Segment g;
+    g.seq = lo;
+    g.row0 = s.row0;
+    g.rows = s.rows;
+    g.start = s.start;
+    long long off = tile - prefix[lo];
+    g.rt = 0;
+    item(s, 0, g.first, g.end, g.tiles);
+    while (off >= static_cast<long long>(g.tiles) * p.st.heads) {
+      off -= static_cast<long long>(g.tiles) * p.st.heads;
+      item(s, ++g.rt, g.first, g.end, g.tiles);
+    }
+    g.h = static_cast<int>(off / g.tiles);
+    g.t0 = static_cast<int>(off % g.tiles);
+    g.id = tile - g.t0;
+    g.t1 = static_cast<int>(min(static_cast<long long>(g.tiles), stop - g.id));
+    return g;
+  }
+};
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+// D[tmem] (+)= A[tmem] B[smem], kind::f16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 128-byte swizzle: rows of 128 bytes, 16-byte units permuted by the row, groups of 8 rows 1024 bytes apart; `lbo`
+// (operands with M or N contiguous only) is the distance of 64-number blocks along M or N.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
+         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+__device__ __forceinline__ void sts16(uint8_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+// Unit (16 bytes) w of row r in a block of 128-byte rows.
+__device__ __forceinline__ int swz(int r, int w) { return r * 128 + ((w ^ (r & 7)) << 4); }
+
+// Writes 8 numbers of a row (words w) to out, in the order of O's columns.
+__device__ __forceinline__ uint4 out_word(const float (&x)[8], float inv, int bf16) {
+  // columns hold dims 0, 4, 1, 5, 2, 6, 3, 7
+  const float y[8] = {x[0] * inv, x[2] * inv, x[4] * inv, x[6] * inv, x[1] * inv, x[3] * inv, x[5] * inv, x[7] * inv};
+  uint32_t r[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (bf16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
+      r[e] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      r[e] = h2u(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
+    }
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(const __grid_constant__ CacheAttnParams p) {
+  using C = PCfg<D>;
+  extern __shared__ uint8_t raw[];
+  PShared<D>& sh = *reinterpret_cast<PShared<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  long long* prefix = reinterpret_cast<long long*>(&sh + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  constexpr int kRowWarps = 4 * C::G, kMmaWarp = kRowWarps + 4;
+  const List<D> list{p, prefix};
+
+  if (warp == kMmaWarp) tmem_alloc(&sh.tmem, C::TMEM);
+  if (tid == 0) {
+    for (int i = 0; i < C::ST; ++i) {
+      mbar_init(&sh.kfull[i], 4);
+      mbar_init(&sh.kempty[i], 1);
+      mbar_init(&sh.vfull[i], 4);
+      mbar_init(&sh.vempty[i], 1);
+    }
+    for (int g = 0; g < C::G; ++g) {
+      mbar_init(&sh.qfull[g], 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sh.pvdone[g][b], 1);
+        mbar_init(&sh.sfull[g][b], 1);
+        mbar_init(&sh.pfull[g][b], 4);
+      }
+    }
+    mbar_init(&sh.drained, 1);
+    fence_barrier_init();
+    sh.abort = 0;
+    sh.scan_total = 0;
+  }
+  // the second half of the extra columns is zero where the first holds all sums (D <= 128)
+  if (D <= 128) {
+    for (int i = tid; i < C::G * 128; i += C::THREADS) sts16(sh.qx[i >> 7] + 128 * 16 + (i & 127) * 16, 0, 0, 0, 0);
+    for (int i = tid; i < C::ST * BT; i += C::THREADS) sts16(sh.kx[i / BT] + BT * 16 + (i % BT) * 16, 0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  for (int base = 0; base < p.st.n_seqs; base += C::THREADS) {
+    const int i = base + tid;
+    const long long n = i < p.st.n_seqs ? list.count(i) : 0;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) sh.wsum[warp] = inc;
+    __syncthreads();
+    long long before = sh.scan_total;
+    for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+    if (i < p.st.n_seqs) prefix[i] = before + inc - n;
+    __syncthreads();
+    if (tid == C::THREADS - 1) sh.scan_total = before + inc;
+    __syncthreads();
+  }
+  const long long T = sh.scan_total;
+  if (tid == 0) prefix[p.st.n_seqs] = T;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // rows that see nothing, and the step's errors
+  for (int i = blockIdx.x; i < p.st.n_seqs; i += gridDim.x) {
+    const SeqSpan s = seq_span(p.st, i);
+    if (s.bad && tid == 0) atomicOr(p.st.err, kErrRange);
+    if (s.live || s.rows == 0) continue;
+    const size_t n = static_cast<size_t>(s.rows) * p.q_heads, at = static_cast<size_t>(s.row0) * p.q_heads;
+    for (size_t e = tid; e < n * (D / 8); e += C::THREADS)
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D + e * 8) = make_uint4(0, 0, 0, 0);
+    if (p.lse != nullptr)
+      for (size_t e = tid; e < n; e += C::THREADS) p.lse[at + e] = -INFINITY;
+  }
+
+  // CTAs with work: at least four tiles each, as what is split has to be joined
+  const long long n = min(static_cast<long long>(gridDim.x), (T + 3) / 4);
+  const bool works = blockIdx.x < n;
+  const long long c0 = works ? T * blockIdx.x / n : 0, c1 = works ? T * (blockIdx.x + 1) / n : 0;
+  volatile int* abort = &sh.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {   // whole warps; false once something gave up
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity & 1))) return true;
+    const bool ok = __all_sync(0xffffffffu, mbar_wait(bar, parity & 1, globaltimer_ns() + p.timeout_ns, abort));
+    if (!ok && lane == 0) {
+      *abort = 1;
+      atomicOr(p.st.err, kErrTimeout);
+    }
+    return ok;
+  };
+
+  if (warp < kRowWarps) {
+    // ------------------------------------------------------------ rows: softmax and output
+    const int g = warp >> 2, r = (warp & 3) * 32 + lane;        // the thread's group and row in it
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t o_at = lanes + C::O_COL + g * D;
+    uint32_t i = 0;                                             // tiles so far: phases of all barriers
+    bool ok = true;
+    for (long long tile = c0; tile < c1 && ok;) {
+      const Segment sg = list.at(tile, c1);
+      tile = sg.id + sg.t1;
+      const int row = sg.rt * C::R + g * 128 + r, total = sg.rows * p.group;
+      const bool there = row < total;
+      const int tok = row / p.group, hq = sg.h * p.group + row % p.group;
+      const int pos = there ? sg.start + tok : -1;
+      const int low = there ? pos - p.window : -1;              // positions at or below it are hidden
+      // the group's first and last row that exist
+      const int row_a = sg.rt * C::R + g * 128, row_b = min(row_a + 128, total) - 1;
+      const int lowest = row_a < total ? sg.start + row_a / p.group : -1;
+      const int highest = row_a < total ? sg.start + row_b / p.group : -1;
+      float f;
+      {
+        // the row as fp16, its largest entry in [1, 2), in the operand's layout; sums over groups, halved
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (sg.row0 + tok) * p.q_tok + static_cast<long long>(hq) * p.q_head;
+        auto word = [&](int w) { return there ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0); };
+        auto two = [&](uint32_t x) {
+          return p.bf16 ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)) : __half22float2(u2h(x));
+        };
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int w = 0; w < D / 8; ++w) {
+          const uint4 a = word(w);
+          const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = two(x[e]);
+            top = max(top, max(__float_as_uint(v.x) & 0x7f800000u, __float_as_uint(v.y) & 0x7f800000u));
+          }
+        }
+        const int ex = static_cast<int>(top >> 23);
+        const int up = min(max(254 - ex, 1), 254);
+        float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
+        f = fmaxf(ldexpf(fabsf(p.scale_log2), 128 - up), 0x1p-120f);   // 2 for the halved keys
+        if (ex == 255) {                                        // a row with inf or NaN is NaN
+          f = __int_as_float(0x7fffffff);
+          scale = 0.0f;
+        }
+        if (p.scale_log2 < 0.0f) scale = -scale;
+        if (p.scale_log2 == 0.0f) scale = 0.0f;
+        __half hi[C::GR], lo[C::GR];
+#pragma unroll
+        for (int gr = 0; gr < C::GR; ++gr) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int w = 4 * gr + k;
+            const uint4 a = word(w);
+            const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 v = two(x[e]);
+              const __half2 h = ex == 255 ? __floats2half2_rn(0.0f, 0.0f) : __floats2half2_rn(v.x * scale, v.y * scale);
+              const float2 b = __half22float2(h);
+              sum += b.x + b.y;
+              y[2 * e] = b.x;
+              y[2 * e + 1] = b.y;
+            }
+            sts16(sh.q[g][w >> 3] + swz(r, w & 7), h2u(__floats2half2_rn(y[0], y[4])), h2u(__floats2half2_rn(y[1], y[5])),
+                  h2u(__floats2half2_rn(y[2], y[6])), h2u(__floats2half2_rn(y[3], y[7])));
+          }
+          sum *= 0.5f;
+          hi[gr] = __float2half_rn(sum);
+          lo[gr] = __float2half_rn(sum - __half2float(hi[gr]));
+        }
+        // 16 columns: the sums' first parts, then their second (D = 256: 8 and 8; else within the first 8)
+        __half cols[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) cols[e] = e < C::GR ? hi[e % C::GR] : e < 2 * C::GR ? lo[e % C::GR] : __float2half(0.0f);
+        const uint32_t* cw = reinterpret_cast<const uint32_t*>(cols);
+        sts16(sh.qx[g] + r * 16, cw[0], cw[1], cw[2], cw[3]);
+        if (D > 128) sts16(sh.qx[g] + 128 * 16 + r * 16, cw[4], cw[5], cw[6], cw[7]);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.qfull[g]);
+      }
+      float m = kNothing, l = 0.0f;
+      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
+        const int buf = i & 1;
+        const uint32_t s_at = lanes + g * 128 + buf * 64;
+        ok = wait(&sh.sfull[g][buf], i >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s0[32], s1[32];
+        tmem_ld32(s_at, s0);
+        tmem_ld32(s_at + 32, s1);
+        tc_wait_ld();
+        const int pos0 = sg.first + t * BT;
+        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 3]);
+        if (pos0 + BT - 1 > lowest || pos0 <= highest - p.window || good != 15) {
+          // hidden scores become -inf: tokens pos - pos0 and later, low - pos0 and earlier, chunks outside the pool
+          const int above = pos - pos0, under = low - pos0;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j > above || j <= under || !((good >> (j / 16)) & 1)) s0[j] = 0xff800000u;
+            if (j + 32 > above || j + 32 <= under || !((good >> (2 + j / 16)) & 1)) s1[j] = 0xff800000u;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          mx[0] = fmaxf(mx[0], __uint_as_float(s0[j]));
+          mx[1] = fmaxf(mx[1], __uint_as_float(s0[j + 1]));
+          mx[2] = fmaxf(mx[2], __uint_as_float(s1[j]));
+          mx[3] = fmaxf(mx[3], __uint_as_float(s1[j + 1]));
+        }
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        const bool passed = top > m + kLag;
+        if (__any_sync(0xffffffffu, passed)) {
+          const float mn = passed ? top : m;
+          const float keep = ex2(m - mn);
+          l *= keep;
+          m = mn;
+          if (t > sg.t0) {                                      // O of this item exists once the tile before is added
+            ok = wait(&sh.pvdone[g][(i - 1) & 1], (i - 1) >> 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              tmem_ld32(o_at + c, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+              tmem_st32(o_at + c, o);
+            }
+          }
+        }
+        uint32_t pr[32];
+        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const float a = ex2(fmaf(__uint_as_float(s0[j]), f, -m)), b = ex2(fmaf(__uint_as_float(s0[j + 1]), f, -m));
+          const float c = ex2(fmaf(__uint_as_float(s1[j]), f, -m)), d = ex2(fmaf(__uint_as_float(s1[j + 1]), f, -m));
+          l4[0] += a;
+          l4[1] += b;
+          l4[2] += c;
+          l4[3] += d;
+          pr[j / 2] = h2u(__floats2half2_rn(a, b));
+          pr[16 + j / 2] = h2u(__floats2half2_rn(c, d));
+        }
+        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        tmem_st32(s_at, pr);
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pfull[g][buf]);
+      }
+      if (!ok) break;
+      // the segment's O: all of the item, or this CTA's part of it
+      // (a barrier for every other tile, as tile i - 1 may or may not be waited for: the tiles two before it are done
+      // for sure when S of tile i is there, so a parity never stands for an older phase)
+      ok = wait(&sh.pvdone[g][(i - 1) & 1], (i - 1) >> 1);
+      if (!ok) break;
+      tc_fence_after();
+      const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
+      const size_t at = static_cast<size_t>(sg.row0 + tok) * p.q_heads + hq;
+      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R) + g * 128 + r;
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(o_at + c, o);
+        tc_wait_ld();
+        if (whole) {
+          if (there) {
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              float x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * w + e]);
+              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(x, inv, p.bf16);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) part[(c + j) * C::R] = __uint_as_float(o[j]);
+        }
+      }
+      tc_fence_before();
+      if (whole) {
+        if (there && p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      } else {
+        part[D * C::R] = m;
+        part[(D + 1) * C::R] = l;
+      }
+    }
+  } else if (warp < kMmaWarp) {
+    // ------------------------------------------------------------ packed tiles to operands
+    const int d = tid - kRowWarps * 32;                         // 0 .. 127
+    long long asked = c0;
+    Segment ahead{};
+    int ahead_t = 0;
+    uint32_t n_asked = 0;
+    bool fresh = true;
+    auto request = [&]() {
+      if (asked < c1) {
+        if (fresh || ahead_t == ahead.t1) {
+          ahead = list.at(asked, c1);
+          ahead_t = ahead.t0;
+          fresh = false;
+        }
+        const uint32_t dst = smem_u32(sh.staging[n_asked % (C::AHEAD + 1)]);
+        constexpr int UC = chunk_bytes(D) / 16;
+#pragma unroll
+        for (int k = 0; k < (C::TILE_BYTES / 16 + 127) / 128; ++k) {
+          const int u = k * 128 + d, ck = u / UC;
+          if (C::TILE_BYTES / 16 % 128 != 0 && u >= C::TILE_BYTES / 16) break;
+          const int pos = ahead.first + ahead_t * BT + ck * kChunkTokens;
+          const uint8_t* src = nullptr;
+          if (pos < ahead.end)
+            src = chunk_at(p.st, __ldg(p.st.table + static_cast<size_t>(ahead.seq) * p.st.stride + (pos >> p.st.page_shift)), pos,
+                           ahead.h, D);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + u * 16),
+                       "l"(src == nullptr ? p.st.pages : src + (u - ck * UC) * 16), "r"(src == nullptr ? 0 : 16)
+                       : "memory");
+        }
+        ++asked;
+        ++ahead_t;
+        ++n_asked;
+      }
+      cp_async_commit();
+    };
+    for (int k = 0; k < C::AHEAD; ++k) request();
+    uint32_t i = 0;
+    bool ok = true;
+    for (long long tile = c0; tile < c1 && ok;) {
+      const Segment sg = list.at(tile, c1);
+      tile = sg.id + sg.t1;
+      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
+        const int st = i % C::ST;
+        const int pos0 = sg.first + t * BT;
+        cp_async_wait<C::AHEAD - 1>();
+        bar_named(1, 128);                                      // the tile is there, and the one before is no longer read
+        request();
+        const uint8_t* tb = sh.staging[i % (C::AHEAD + 1)];
+        if (i >= C::ST) ok = wait(&sh.kempty[st], i / C::ST - 1);
+        ok = bar_any(2, 128, !ok) ? false : true;
+        if (!ok) break;
+        if (d < BT / kChunkTokens) {
+          const int pos = pos0 + d * kChunkTokens;
+          bool in = pos < sg.end;
+          if (in) {
+            in = static_cast<unsigned>(__ldg(p.st.table + static_cast<size_t>(sg.seq) * p.st.stride + (pos >> p.st.page_shift))) <
+                 static_cast<unsigned>(p.st.n_pages);
+            if (!in) atomicOr(p.st.err, kErrRange);
+          }
+          const unsigned all = __ballot_sync((1u << (BT / kChunkTokens)) - 1, in);
+          if (d == 0) sh.good[i & 3] = static_cast<int>(all);
+        }
+        // K: 16 bytes of codes at a time; rows r and r + 4 in neighbouring quarter warps fill all banks
+#pragma unroll
+        for (int k = 0; k < BT * (D / 32) / 128; ++k) {
+          constexpr int UR = D / 32;                            // units of a row
+          const int u = k * 128 + d, q = u / UR, c = u % UR;
+          const int row = UR == 4 ? (q & ~7) | ((q & 1) << 2) | ((q >> 1) & 3) : q;
+          const uint8_t* ch = tb + (row >> 4) * chunk_bytes(D);
+          const uint4 cw = *reinterpret_cast<const uint4*>(ch + (row & 15) * (D / 2) + c * 16);
+          const uint32_t w4[4] = {cw.x, cw.y, cw.z, cw.w};
+          const uint32_t* prs = reinterpret_cast<const uint32_t*>(ch + 8 * D + (row & 15) * (D / 8));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int place = 4 * c + e, gr = place % C::GR, w = 4 * gr + place / C::GR;
+            const __half2 s2 = __low2half2(u2h(prs[gr]));
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int n4 = 0; n4 < 4; ++n4) {
+              // (c - 8) / 2, exact: 512 + c / 2 in place 0, 32 + c / 2 in place 1
+              const uint32_t x = n4 & 2 ? w4[e] >> 8 : w4[e];
+              const __half2 c2 = n4 & 1 ? __hadd2(u2h(and_or(x, 0x00f000f0u, 0x50005000u)), u2h(0xd080d080u))     // - 36
+                                        : __hadd2(u2h(and_or(x, 0x000f000fu, 0x60006000u)), u2h(0xe008e008u));    // - 516
+              const __half2 h = __hmul2(c2, s2);
+              hi[n4] = h2u(h);
+              lo[n4] = h2u(__hfma2(c2, s2, __hneg2(h)));
+            }
+            sts16(sh.khi[st][w >> 3] + swz(row, w & 7), hi[0], hi[1], hi[2], hi[3]);
+            sts16(sh.klo[st][w >> 3] + swz(row, w & 7), lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        if (d < BT) {                                           // the b of a token's groups, twice
+          const uint32_t* prs = reinterpret_cast<const uint32_t*>(tb + (d >> 4) * chunk_bytes(D) + 8 * D + (d & 15) * (D / 8));
+          uint32_t b[4];
+          if constexpr (D == 64) {
+            b[0] = __byte_perm(prs[0], prs[1], 0x7632);
+            b[1] = b[0];
+            b[2] = b[3] = 0;
+          } else if constexpr (D == 128) {
+            b[0] = b[2] = __byte_perm(prs[0], prs[1], 0x7632);
+            b[1] = b[3] = __byte_perm(prs[2], prs[3], 0x7632);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) b[e] = __byte_perm(prs[2 * e], prs[2 * e + 1], 0x7632);
+            sts16(sh.kx[st] + BT * 16 + d * 16, b[0], b[1], b[2], b[3]);
+          }
+          sts16(sh.kx[st] + d * 16, b[0], b[1], b[2], b[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kfull[st]);
+        if (i >= C::ST) ok = wait(&sh.vempty[st], i / C::ST - 1);
+        ok = bar_any(2, 128, !ok) ? false : true;
+        if (!ok) break;
+        // V: rows of tokens as they are; tokens behind the item's context become zeros
+#pragma unroll
+        for (int k = 0; k < BT * (D / 32) / 128; ++k) {
+          constexpr int UR = D / 32;
+          const int u = k * 128 + d, q = u / UR, c = u % UR;
+          const int pr = UR == 4 ? (q & ~15) | ((q & 1) << 3) | ((q >> 1) & 7) : q;   // rows p and p + 8: tokens 2 p, 2 p + 1
+          const int row = (pr & ~15) | ((pr & 7) * 2 + ((pr >> 3) & 1));              // the token
+          const uint8_t* ch = tb + (pr >> 4) * chunk_bytes(D) + 10 * D;
+          const uint4 cw = *reinterpret_cast<const uint4*>(ch + (pr & 15) * (D / 2) + c * 16);
+          const uint32_t w4[4] = {cw.x, cw.y, cw.z, cw.w};
+          const uint32_t* prs = reinterpret_cast<const uint32_t*>(ch + 8 * D + (pr & 15) * (D / 8));
+          const bool live = pos0 + row < sg.end;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int place = 4 * c + e, w = place / C::H + 8 * (place % C::H);       // C::H = D / 64
+            const int gr = w >> 2, pp = (gr & 1) * C::H + (gr >> 1);
+            const uint32_t sb = live ? prs[pp] : 0;
+            const __half2 s2 = __low2half2(u2h(sb)), b2 = __high2half2(u2h(sb));
+            uint32_t x4[4];
+#pragma unroll
+            for (int n4 = 0; n4 < 4; ++n4) {
+              const uint32_t x = n4 & 2 ? w4[e] >> 8 : w4[e];
+              const __half2 c2 = n4 & 1 ? __hadd2(u2h(and_or(x, 0x00f000f0u, 0x54005400u)), u2h(0xd480d480u))     // - 72
+                                        : __hadd2(u2h(and_or(x, 0x000f000fu, 0x64006400u)), u2h(0xe408e408u));    // - 1032
+              x4[n4] = h2u(__hfma2(c2, s2, b2));
+            }
+            sts16(sh.v[st][w >> 3] + swz(row, w & 7), x4[0], x4[1], x4[2], x4[3]);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.vfull[st]);
+      }
+    }
+    cp_async_wait<0>();
+  } else {
+    // ------------------------------------------------------------ products
+    constexpr uint32_t kIdS = make_idesc(1u, 0u, 0u, 128u, BT);
+    constexpr uint32_t kIdO = make_idesc(1u, 0u, 0u, 128u, D) | 1u << 16;   // B with N contiguous
+    uint32_t i = 0, segs = 0;
+    bool ok = true;
+    auto add_values = [&](uint32_t j, bool begin) {             // O += P V of tile j
+      const int st = j % C::ST, buf = j & 1;
+      ok = wait(&sh.vfull[st], j / C::ST);
+      for (int g = 0; g < C::G && ok; ++g) {
+        ok = wait(&sh.pfull[g][buf], j >> 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t a = tmem + g * 128 + buf * 64, o = tmem + C::O_COL + g * D;
+          const uint32_t vb = smem_u32(sh.v[st][0]);
+#pragma unroll
+          for (int k = 0; k < BT / 16; ++k)
+            mma_f16_ts(o, a + k * 8, desc_sw128(vb + k * 2048, BT * 128), kIdO, begin && k == 0 ? 0u : 1u);
+          tc_commit(&sh.pvdone[g][buf]);
+          if (g == C::G - 1) tc_commit(&sh.vempty[st]);
+        }
+        __syncwarp();
+      }
+    };
+    for (long long tile = c0; tile < c1 && ok; ++segs) {
+      const Segment sg = list.at(tile, c1);
+      tile = sg.id + sg.t1;
+      for (int g = 0; g < C::G && ok; ++g) ok = wait(&sh.qfull[g], segs);
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
+        const int st = i % C::ST, buf = i & 1;
+        ok = wait(&sh.kfull[st], i / C::ST);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t hb = smem_u32(sh.khi[st][0]), lb = smem_u32(sh.klo[st][0]);
+          for (int g = 0; g < C::G; ++g) {
+            const uint32_t s = tmem + g * 128 + buf * 64, qb = smem_u32(sh.q[g][0]);
+            // smallest parts first: b sum q, then the remainders, then the rest
+            mma_f16_ss(s, smem_desc_noswizzle(smem_u32(sh.qx[g]), 128 * 16, 128), smem_desc_noswizzle(smem_u32(sh.kx[st]), BT * 16, 128),
+                       kIdS, 0u);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_f16_ss(s, desc_sw128(qb + (k >> 2) * 128 * 128 + (k & 3) * 32, 16), desc_sw128(lb + (k >> 2) * BT * 128 + (k & 3) * 32, 16),
+                         kIdS, 1u);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              mma_f16_ss(s, desc_sw128(qb + (k >> 2) * 128 * 128 + (k & 3) * 32, 16), desc_sw128(hb + (k >> 2) * BT * 128 + (k & 3) * 32, 16),
+                         kIdS, 1u);
+            tc_commit(&sh.sfull[g][buf]);
+          }
+          tc_commit(&sh.kempty[st]);
+        }
+        __syncwarp();
+        if (t > sg.t0) add_values(i - 1, t - 1 == sg.t0);
+      }
+      if (ok) add_values(i - 1, sg.t1 - 1 == sg.t0);
+    }
+    if (lane == 0) tc_commit(&sh.drained);
+    __syncwarp();
+    mbar_wait(&sh.drained, 0, globaltimer_ns() + p.timeout_ns, nullptr);   // no product in flight below
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, C::TMEM);
+  if (!works || sh.abort) return;
+
+  // Count this CTA's parts (of the item that began before it, of the one that goes on behind it); the CTA that counts
+  // an item's last one adds them up in their order.
+  auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * n - 1) / T); };
+  if (tid < 2) {
+    sh.last[tid] = 0;
+    const Segment sg = list.at(tid == 0 ? c0 : c1 - 1, c1);
+    // tid 0: the item at the range's begin, if it began before; tid 1: the one at its end, if it began here and goes on
+    const bool mine = tid == 0 ? sg.id < c0 : sg.id >= c0 && sg.id + sg.tiles > c1;
+    if (mine) {
+      const int f0 = cta_of(sg.id), f1 = cta_of(sg.id + sg.tiles - 1);
+      if (atom_add_acq_rel_gpu(p.cnt + f0, 1u) == static_cast<uint32_t>(f1 - f0)) {
+        sh.last[tid] = 1;
+        p.cnt[f0] = 0;
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int it = 0; it < 2; ++it) {
+    if (!sh.last[it]) continue;
+    const Segment sg = list.at(it == 0 ? c0 : c1 - 1, c1);
+    const int f0 = cta_of(sg.id), parts = cta_of(sg.id + sg.tiles - 1) - f0 + 1;
+    if (tid >= C::R) continue;
+    const int row = sg.rt * C::R + tid;
+    if (row >= sg.rows * p.group) continue;
+    auto part_of = [&](int x) { return p.part + static_cast<size_t>((f0 + x) * 2 + (x == 0 ? 1 : 0)) * ((D + 2) * C::R) + tid; };
+    float m = kNothing, l = 0.0f;
+    for (int x = 0; x < parts; ++x) m = fmaxf(m, part_of(x)[D * C::R]);
+    for (int x = 0; x < parts; ++x) l = fmaf(ex2(part_of(x)[D * C::R] - m), part_of(x)[(D + 1) * C::R], l);
+    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+    const size_t at = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+#pragma unroll 1
+      for (int x = 0; x < parts; ++x) {
+        const float* f = part_of(x);
+        const float w = ex2(f[D * C::R] - m);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = fmaf(w, f[(c + j) * C::R], o[j]);
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = o[8 * w + e];
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(x, inv, p.bf16);
+      }
+    }
+    if (p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+  }
+}
+
+template <int D>
+cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
+  constexpr int kMost = static_cast<int>(sizeof(PShared<D>) + 1024 + (kCacheMaxSeqs + 1) * 8);
+  static_assert(sizeof(PShared<D>) + 1024 + 8 <= 227 * 1024, "shared memory");
+  constexpr int kCap = kMost < 227 * 1024 ? kMost : 227 * 1024;
+  static std::atomic<unsigned long long> set{0};   // devices whose attribute is set
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (bit == 0 || !(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(cache_prefill_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCap);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cache_prefill_kernel<D><<<p.grid, PCfg<D>::THREADS, cache_prefill_smem(D, p.st.n_seqs), stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t cache_prefill_smem(int dim, int n_seqs) {
+  const size_t fixed = dim == 64 ? sizeof(PShared<64>) : dim == 128 ? sizeof(PShared<128>) : sizeof(PShared<256>);
+  return fixed + 1024 + (static_cast<size_t>(n_seqs) + 1) * 8;
+}
+size_t cache_prefill_part_floats(int dim) { return static_cast<size_t>(dim + 2) * (dim == 256 ? PCfg<256>::R : PCfg<128>::R); }
+cudaError_t launch_cache_prefill(const CacheAttnParams& p, int dim, cudaStream_t stream) {
+  return dim == 64 ? launch_as<64>(p, stream) : dim == 128 ? launch_as<128>(p, stream) : launch_as<256>(p, stream);
+}
+
+}  // namespace bs
