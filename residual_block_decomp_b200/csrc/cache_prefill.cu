@@ -3,9 +3,9 @@
 // list of tiles and how it is split).
 //
 // With hundreds of query rows the products bound the time, so they run on tcgen05: an item is one (sequence, head,
-// tile of up to 256 query rows), its context is taken in tiles of 64 tokens, and a tile's packed bytes are expanded
-// once in shared memory for all rows.  Per tile and group of 128 rows
-//     S = Q K^T   (M = 128, N = 64, shared memory operands, fp32 in tensor memory)
+// tile of up to 256 query rows), its context is taken in tiles of 128 tokens (D = 256: 128 rows, 64 tokens), and a
+// tile's packed bytes are expanded once in shared memory for all rows.  Per tile and group of 128 rows
+//     S = Q K^T   (M = 128, N = 128, shared memory operands, fp32 in tensor memory)
 //     P = 2^(S f - m) as fp16, written over S in tensor memory
 //     O += P V    (A from tensor memory, B = V with the dims contiguous)
 // with the maximum and sum of a row in the registers of the thread that owns it.  As in the kernel for few rows the
@@ -18,9 +18,11 @@
 // as the rounding of P does, and the lse, which is fp32, by more than fp32 allows.  Values are rounded to fp16 by
 // one fma.
 //
-// Roles: 4 warps a group own its rows (softmax, output); 4 warps copy packed tiles ahead and expand them
-// (K and V stages); one thread issues all products: S of tile t before O of tile t - 1, so the tensor pipe has
-// work while the rows' threads are at tile t.
+// Roles: 4 warps a group own its rows (softmax, output); 8 warps copy packed tiles ahead and expand them; one thread
+// issues all products.  The two groups take turns on the tensor pipe: while one's rows are at their softmax the other's
+// products run (PV of tile t - 1, then S of tile t, group after group).  128 tokens a product (and not 64) because an
+// operand from shared memory is read at 128 bytes a clock: at N = 64 reading Q again for every 64 tokens
+// takes longer than multiplying.
 //
 // 8 numbers of a word are kept in the order (0, 4, 1, 5, 2, 6, 3, 7) that unpacking gives, in Q and K alike (a sum
 // does not mind), and in V as the order of O's columns, undone where rows are written.
@@ -35,40 +37,44 @@
 namespace bs {
 namespace {
 
-constexpr int BT = 64;                  // tokens of a tile
 constexpr float kNothing = -3.0e38f;    // the reference before any score
 constexpr float kLag = 8.0f;            // how far scores may pass it
 
 template <int D>
 struct PCfg {
-  static constexpr int G = D == 256 ? 1 : 2;               // groups of 128 rows (tensor memory: 128 + D columns each)
+  static constexpr int G = D == 256 ? 1 : 2;               // groups of 128 rows
   static constexpr int R = 128 * G;
-  static constexpr int ST = D == 256 ? 1 : 2;              // K and V stages
-  static constexpr int AHEAD = D == 256 ? 1 : 2;           // packed tiles requested ahead of the one in use
-  static constexpr int H = D / 64;                         // 128-byte columns blocks of a row
+  static constexpr int BT = D == 256 ? 64 : 128;           // tokens of a tile
+  static constexpr int NB = D == 256 ? 2 : 1;              // buffers of S: a single group alternates between two
+  static constexpr int ST = D == 64 ? 2 : 1;               // K and V stages
+  static constexpr int AHEAD = 1;                          // packed tiles requested ahead of the one in use
+  static constexpr int H = D / 64;                         // 128-byte column blocks of a row
   static constexpr int GR = D / 32;
-  static constexpr int TILE_BYTES = BT / kChunkTokens * chunk_bytes(D);
-  static constexpr int THREADS = G * 128 + 128 + 32;
-  static constexpr int O_COL = G * 128;                    // tensor memory columns: S of group g, buffer b at 128 g + 64 b
+  static constexpr int CHUNKS = BT / kChunkTokens;
+  static constexpr int TILE_BYTES = CHUNKS * chunk_bytes(D);
+  static constexpr int XW = 8, XT = XW * 32;               // expanding warps, threads
+  static constexpr int THREADS = G * 128 + XT + 32;
+  static constexpr int O_COL = G * NB * BT;                // tensor memory columns: S first (BT each), then O (D each)
   static constexpr uint32_t TMEM = 512;
+  static_assert(O_COL + G * D <= 512, "tensor memory");
 };
 
 template <int D>
 struct alignas(1024) PShared {
   using C = PCfg<D>;
   uint8_t q[C::G][C::H][128 * 128];     // 128-byte swizzled rows
-  uint8_t khi[C::ST][C::H][BT * 128];
-  uint8_t klo[C::ST][C::H][BT * 128];
-  uint8_t v[C::ST][C::H][BT * 128];
+  uint8_t khi[C::ST][C::H][C::BT * 128];
+  uint8_t klo[C::ST][C::H][C::BT * 128];
+  uint8_t v[C::ST][C::H][C::BT * 128];
   uint8_t qx[C::G][128 * 32];           // the 16 columns of sums and of b: core matrices of 8 rows x 16 bytes
-  uint8_t kx[C::ST][BT * 32];
+  uint8_t kx[C::ST][C::BT * 32];
   uint8_t staging[C::AHEAD + 1][C::TILE_BYTES];
   uint64_t kfull[C::ST], kempty[C::ST], vfull[C::ST], vempty[C::ST];
-  uint64_t qfull[C::G], sfull[C::G][2], pfull[C::G][2], pvdone[C::G][2], drained;
-  long long scan_total, wsum[16];
+  uint64_t qfull[C::G], sfull[C::G][C::NB], pfull[C::G][C::NB], pvdone[C::G][2], drained;
+  long long scan_total, wsum[32];
   uint32_t tmem;
   int abort, last[2];
-  int good[4];                          // chunks of tile i % 4 that are in the pool
+  int good[8];                          // chunks of tile i % 8 that are in the pool
   // then long long prefix[n_seqs + 1]
 };
 
@@ -93,7 +99,7 @@ struct List {
     const int lowest = s.start + rt * C::R / p.group;
     end = s.start + (min((rt + 1) * C::R, total) - 1) / p.group + 1;
     first = lowest >= p.window ? (lowest - p.window + 1) / kChunkTokens * kChunkTokens : 0;
-    tiles = (end - first + BT - 1) / BT;
+    tiles = (end - first + C::BT - 1) / C::BT;
   }
   __device__ long long count(int i) const {
     const SeqSpan s = seq_span(p.st, i);
@@ -148,20 +154,39 @@ __device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t m
   asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
   return r;
 }
-// D[tmem] (+)= A[tmem] B[smem], kind::f16.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
+// Products of one tile are issued by one thread at a rate that counts, so descriptors are taken as their low words
+// (address and leading offset); the high words are constants.
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
       : "memory");
 }
-// 128-byte swizzle: rows of 128 bytes, 16-byte units permuted by the row, groups of 8 rows 1024 bytes apart; `lbo`
-// (operands with M or N contiguous only) is the distance of 64-number blocks along M or N.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr, uint32_t lbo) {
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16 |
-         static_cast<uint64_t>(1024 >> 4) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "n"(HI)
+      : "memory");
+}
+// 128-byte swizzle: rows of 128 bytes, 16-byte units permuted by the row, groups of 8 rows 1024 bytes apart (high
+// word); `lbo` (operands with M or N contiguous only) is the distance of 64-number blocks along M or N.
+constexpr uint32_t kSw128 = 1024 >> 4 | 1u << 14 | 2u << 29;
+// No swizzle: core matrices of 8 rows x 16 bytes, along M or N 128 bytes apart (high word), along K `lbo`.
+constexpr uint32_t kPlain = 128 >> 4 | 1u << 14;
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) {
+  return ((addr >> 4) & 0x3FFFu) | (lbo >> 4) << 16;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 __device__ __forceinline__ void sts16(uint8_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
@@ -193,21 +218,21 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
   PShared<D>& sh = *reinterpret_cast<PShared<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   long long* prefix = reinterpret_cast<long long*>(&sh + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kRowWarps = 4 * C::G, kMmaWarp = kRowWarps + 4;
+  constexpr int kRowWarps = 4 * C::G, kMmaWarp = kRowWarps + C::XW, BT = C::BT;
   const List<D> list{p, prefix};
 
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, C::TMEM);
   if (tid == 0) {
     for (int i = 0; i < C::ST; ++i) {
-      mbar_init(&sh.kfull[i], 4);
+      mbar_init(&sh.kfull[i], C::XW);
       mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.vfull[i], 4);
+      mbar_init(&sh.vfull[i], C::XW);
       mbar_init(&sh.vempty[i], 1);
     }
     for (int g = 0; g < C::G; ++g) {
       mbar_init(&sh.qfull[g], 4);
-      for (int b = 0; b < 2; ++b) {
-        mbar_init(&sh.pvdone[g][b], 1);
+      for (int b = 0; b < 2; ++b) mbar_init(&sh.pvdone[g][b], 1);
+      for (int b = 0; b < C::NB; ++b) {
         mbar_init(&sh.sfull[g][b], 1);
         mbar_init(&sh.pfull[g][b], 4);
       }
@@ -362,33 +387,31 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       }
       float m = kNothing, l = 0.0f;
       for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int buf = i & 1;
-        const uint32_t s_at = lanes + g * 128 + buf * 64;
-        ok = wait(&sh.sfull[g][buf], i >> 1);
+        const int buf = i % C::NB;
+        const uint32_t s_at = lanes + (g * C::NB + buf) * BT;
+        ok = wait(&sh.sfull[g][buf], i / C::NB);
         if (!ok) break;
         tc_fence_after();
-        uint32_t s0[32], s1[32];
-        tmem_ld32(s_at, s0);
-        tmem_ld32(s_at + 32, s1);
-        tc_wait_ld();
         const int pos0 = sg.first + t * BT;
-        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 3]);
-        if (pos0 + BT - 1 > lowest || pos0 <= highest - p.window || good != 15) {
-          // hidden scores become -inf: tokens pos - pos0 and later, low - pos0 and earlier, chunks outside the pool
-          const int above = pos - pos0, under = low - pos0;
+        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 7]);
+        const bool masked = pos0 + BT - 1 > lowest || pos0 <= highest - p.window || good != (1 << C::CHUNKS) - 1;
+        // 32 scores at a time, twice: for the maximum, and for the weights.  Hidden scores become -inf: tokens
+        // behind the row's own, those the window leaves out, chunks outside the pool.
+        const int above = pos - pos0, under = low - pos0;
+        auto hide = [&](uint32_t (&x)[32], int c) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j > above || j <= under || !((good >> (j / 16)) & 1)) s0[j] = 0xff800000u;
-            if (j + 32 > above || j + 32 <= under || !((good >> (2 + j / 16)) & 1)) s1[j] = 0xff800000u;
-          }
-        }
+          for (int j = 0; j < 32; ++j)
+            if (c + j > above || c + j <= under || !((good >> (c / 16 + j / 16)) & 1)) x[j] = 0xff800000u;
+        };
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t x[32];
+#pragma unroll 1
+        for (int c = 0; c < BT; c += 32) {
+          tmem_ld32(s_at + c, x);
+          tc_wait_ld();
+          if (masked) hide(x, c);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          mx[0] = fmaxf(mx[0], __uint_as_float(s0[j]));
-          mx[1] = fmaxf(mx[1], __uint_as_float(s0[j + 1]));
-          mx[2] = fmaxf(mx[2], __uint_as_float(s1[j]));
-          mx[3] = fmaxf(mx[3], __uint_as_float(s1[j + 1]));
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
         }
         const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         const bool passed = top > m + kLag;
@@ -403,30 +426,31 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(o_at + c, o);
+              tmem_ld32(o_at + c, x);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-              tmem_st32(o_at + c, o);
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * keep);
+              tmem_st32(o_at + c, x);
             }
           }
         }
-        uint32_t pr[32];
         float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+        for (int c = 0; c < BT; c += 32) {
+          tmem_ld32(s_at + c, x);
+          tc_wait_ld();
+          if (masked) hide(x, c);
+          uint32_t pr[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float a = ex2(fmaf(__uint_as_float(s0[j]), f, -m)), b = ex2(fmaf(__uint_as_float(s0[j + 1]), f, -m));
-          const float c = ex2(fmaf(__uint_as_float(s1[j]), f, -m)), d = ex2(fmaf(__uint_as_float(s1[j + 1]), f, -m));
-          l4[0] += a;
-          l4[1] += b;
-          l4[2] += c;
-          l4[3] += d;
-          pr[j / 2] = h2u(__floats2half2_rn(a, b));
-          pr[16 + j / 2] = h2u(__floats2half2_rn(c, d));
+          for (int j = 0; j < 32; j += 2) {
+            const float a = ex2(fmaf(__uint_as_float(x[j]), f, -m)), b = ex2(fmaf(__uint_as_float(x[j + 1]), f, -m));
+            l4[j & 2] += a;
+            l4[(j & 2) + 1] += b;
+            pr[j / 2] = h2u(__floats2half2_rn(a, b));
+          }
+          tmem_st16(s_at + c / 2, pr);                          // over scores that have been read
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        tmem_st32(s_at, pr);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -473,40 +497,50 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------ packed tiles to operands
-    const int d = tid - kRowWarps * 32;                         // 0 .. 127
-    long long asked = c0;
+    const int d = tid - kRowWarps * 32;                         // 0 .. XT - 1
+    // The next tile to request, and in lane m the table's entry for its chunk m, loaded a tile earlier.
+    long long next = c0;
     Segment ahead{};
-    int ahead_t = 0;
+    int ahead_t = 0, entry = 0;
     uint32_t n_asked = 0;
-    bool fresh = true;
+    auto look = [&]() {
+      if (next >= c1) return;
+      if (next == c0 || ahead_t == ahead.t1) {
+        ahead = list.at(next, c1);
+        ahead_t = ahead.t0;
+      }
+      const int pos = ahead.first + ahead_t * BT + lane * kChunkTokens;
+      entry = lane < C::CHUNKS && pos < ahead.end
+                  ? __ldg(p.st.table + static_cast<size_t>(ahead.seq) * p.st.stride + (pos >> p.st.page_shift)) : -1;
+    };
     auto request = [&]() {
-      if (asked < c1) {
-        if (fresh || ahead_t == ahead.t1) {
-          ahead = list.at(asked, c1);
-          ahead_t = ahead.t0;
-          fresh = false;
-        }
+      if (next < c1) {
+        const int pos = ahead.first + ahead_t * BT + lane * kChunkTokens;
+        const bool wanted = lane < C::CHUNKS && pos < ahead.end;
+        const uint8_t* mine = wanted ? chunk_at(p.st, entry, pos, ahead.h, D) : nullptr;
+        const unsigned there = __ballot_sync(0xffffffffu, mine != nullptr);
+        if (d == 0) sh.good[n_asked & 7] = static_cast<int>(there);
+        if (wanted && mine == nullptr && d < 32) atomicOr(p.st.err, kErrRange);
         const uint32_t dst = smem_u32(sh.staging[n_asked % (C::AHEAD + 1)]);
-        constexpr int UC = chunk_bytes(D) / 16;
+        constexpr int UC = chunk_bytes(D) / 16, UNITS = C::TILE_BYTES / 16;
 #pragma unroll
-        for (int k = 0; k < (C::TILE_BYTES / 16 + 127) / 128; ++k) {
-          const int u = k * 128 + d, ck = u / UC;
-          if (C::TILE_BYTES / 16 % 128 != 0 && u >= C::TILE_BYTES / 16) break;
-          const int pos = ahead.first + ahead_t * BT + ck * kChunkTokens;
-          const uint8_t* src = nullptr;
-          if (pos < ahead.end)
-            src = chunk_at(p.st, __ldg(p.st.table + static_cast<size_t>(ahead.seq) * p.st.stride + (pos >> p.st.page_shift)), pos,
-                           ahead.h, D);
+        for (int k = 0; k < (UNITS + C::XT - 1) / C::XT; ++k) {
+          const int u = k * C::XT + d, ck = min(u / UC, C::CHUNKS - 1);
+          const unsigned long long base = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), ck);
+          if (UNITS % C::XT != 0 && u >= UNITS) continue;
+          const bool in = base != 0;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + u * 16),
-                       "l"(src == nullptr ? p.st.pages : src + (u - ck * UC) * 16), "r"(src == nullptr ? 0 : 16)
+                       "l"(in ? reinterpret_cast<const uint8_t*>(base) + (u - ck * UC) * 16 : p.st.pages), "r"(in ? 16 : 0)
                        : "memory");
         }
-        ++asked;
+        ++next;
         ++ahead_t;
         ++n_asked;
+        look();
       }
       cp_async_commit();
     };
+    look();
     for (int k = 0; k < C::AHEAD; ++k) request();
     uint32_t i = 0;
     bool ok = true;
@@ -517,28 +551,17 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         const int st = i % C::ST;
         const int pos0 = sg.first + t * BT;
         cp_async_wait<C::AHEAD - 1>();
-        bar_named(1, 128);                                      // the tile is there, and the one before is no longer read
+        bar_named(1, C::XT);                                    // the tile is there, and the one before is no longer read
         request();
         const uint8_t* tb = sh.staging[i % (C::AHEAD + 1)];
         if (i >= C::ST) ok = wait(&sh.kempty[st], i / C::ST - 1);
-        ok = bar_any(2, 128, !ok) ? false : true;
+        ok = !bar_any(2, C::XT, !ok);
         if (!ok) break;
-        if (d < BT / kChunkTokens) {
-          const int pos = pos0 + d * kChunkTokens;
-          bool in = pos < sg.end;
-          if (in) {
-            in = static_cast<unsigned>(__ldg(p.st.table + static_cast<size_t>(sg.seq) * p.st.stride + (pos >> p.st.page_shift))) <
-                 static_cast<unsigned>(p.st.n_pages);
-            if (!in) atomicOr(p.st.err, kErrRange);
-          }
-          const unsigned all = __ballot_sync((1u << (BT / kChunkTokens)) - 1, in);
-          if (d == 0) sh.good[i & 3] = static_cast<int>(all);
-        }
         // K: 16 bytes of codes at a time; rows r and r + 4 in neighbouring quarter warps fill all banks
 #pragma unroll
-        for (int k = 0; k < BT * (D / 32) / 128; ++k) {
+        for (int k = 0; k < BT * (D / 32) / C::XT; ++k) {
           constexpr int UR = D / 32;                            // units of a row
-          const int u = k * 128 + d, q = u / UR, c = u % UR;
+          const int u = k * C::XT + d, q = u / UR, c = u % UR;
           const int row = UR == 4 ? (q & ~7) | ((q & 1) << 2) | ((q >> 1) & 3) : q;
           const uint8_t* ch = tb + (row >> 4) * chunk_bytes(D);
           const uint4 cw = *reinterpret_cast<const uint4*>(ch + (row & 15) * (D / 2) + c * 16);
@@ -584,13 +607,13 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.kfull[st]);
         if (i >= C::ST) ok = wait(&sh.vempty[st], i / C::ST - 1);
-        ok = bar_any(2, 128, !ok) ? false : true;
+        ok = !bar_any(2, C::XT, !ok);
         if (!ok) break;
         // V: rows of tokens as they are; tokens behind the item's context become zeros
 #pragma unroll
-        for (int k = 0; k < BT * (D / 32) / 128; ++k) {
+        for (int k = 0; k < BT * (D / 32) / C::XT; ++k) {
           constexpr int UR = D / 32;
-          const int u = k * 128 + d, q = u / UR, c = u % UR;
+          const int u = k * C::XT + d, q = u / UR, c = u % UR;
           const int pr = UR == 4 ? (q & ~15) | ((q & 1) << 3) | ((q >> 1) & 7) : q;   // rows p and p + 8: tokens 2 p, 2 p + 1
           const int row = (pr & ~15) | ((pr & 7) * 2 + ((pr >> 3) & 1));              // the token
           const uint8_t* ch = tb + (pr >> 4) * chunk_bytes(D) + 10 * D;
@@ -627,57 +650,59 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     constexpr uint32_t kIdO = make_idesc(1u, 0u, 0u, 128u, D) | 1u << 16;   // B with N contiguous
     uint32_t i = 0, segs = 0;
     bool ok = true;
-    auto add_values = [&](uint32_t j, bool begin) {             // O += P V of tile j
-      const int st = j % C::ST, buf = j & 1;
-      ok = wait(&sh.vfull[st], j / C::ST);
-      for (int g = 0; g < C::G && ok; ++g) {
-        ok = wait(&sh.pfull[g][buf], j >> 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t a = tmem + g * 128 + buf * 64, o = tmem + C::O_COL + g * D;
-          const uint32_t vb = smem_u32(sh.v[st][0]);
+    auto add_values = [&](int g, uint32_t j, bool begin) {      // O += P V of tile j
+      const int st = j % C::ST, buf = j % C::NB;
+      if (g == 0) ok = wait(&sh.vfull[st], j / C::ST);
+      if (ok) ok = wait(&sh.pfull[g][buf], j / C::NB);
+      if (!ok) return;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t a = tmem + (g * C::NB + buf) * BT, o = tmem + C::O_COL + g * D;
+        const uint32_t vb = desc_lo(smem_u32(sh.v[st][0]), BT * 128);
 #pragma unroll
-          for (int k = 0; k < BT / 16; ++k)
-            mma_f16_ts(o, a + k * 8, desc_sw128(vb + k * 2048, BT * 128), kIdO, begin && k == 0 ? 0u : 1u);
-          tc_commit(&sh.pvdone[g][buf]);
-          if (g == C::G - 1) tc_commit(&sh.vempty[st]);
-        }
-        __syncwarp();
+        for (int k = 0; k < BT / 16; ++k) mma_ts<kSw128>(o, a + k * 8, vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
+        tc_commit(&sh.pvdone[g][j & 1]);
+        if (g == C::G - 1) tc_commit(&sh.vempty[st]);
       }
+      __syncwarp();
+    };
+    auto scores = [&](int g) {                                  // S of tile i
+      const int st = i % C::ST, buf = i % C::NB;
+      if (g == 0) ok = wait(&sh.kfull[st], i / C::ST);
+      if (!ok) return;
+      tc_fence_after();
+      if (lane == 0) {
+        const uint32_t hb = desc_lo(smem_u32(sh.khi[st][0]), 16), lb = desc_lo(smem_u32(sh.klo[st][0]), 16);
+        const uint32_t s = tmem + (g * C::NB + buf) * BT, qb = desc_lo(smem_u32(sh.q[g][0]), 16);
+        // smallest parts first: b sum q, then the remainders, then the rest
+        mma_ss<kPlain>(s, desc_lo(smem_u32(sh.qx[g]), 128 * 16), desc_lo(smem_u32(sh.kx[st]), BT * 16), kIdS, 0u);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss<kSw128>(s, qb + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4), lb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+          mma_ss<kSw128>(s, qb + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4), hb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
+        tc_commit(&sh.sfull[g][buf]);
+        if (g == C::G - 1) tc_commit(&sh.kempty[st]);
+      }
+      __syncwarp();
     };
     for (long long tile = c0; tile < c1 && ok; ++segs) {
       const Segment sg = list.at(tile, c1);
       tile = sg.id + sg.t1;
       for (int g = 0; g < C::G && ok; ++g) ok = wait(&sh.qfull[g], segs);
+#pragma unroll 1
       for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
-        const int st = i % C::ST, buf = i & 1;
-        ok = wait(&sh.kfull[st], i / C::ST);
-        if (!ok) break;
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t hb = smem_u32(sh.khi[st][0]), lb = smem_u32(sh.klo[st][0]);
-          for (int g = 0; g < C::G; ++g) {
-            const uint32_t s = tmem + g * 128 + buf * 64, qb = smem_u32(sh.q[g][0]);
-            // smallest parts first: b sum q, then the remainders, then the rest
-            mma_f16_ss(s, smem_desc_noswizzle(smem_u32(sh.qx[g]), 128 * 16, 128), smem_desc_noswizzle(smem_u32(sh.kx[st]), BT * 16, 128),
-                       kIdS, 0u);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_f16_ss(s, desc_sw128(qb + (k >> 2) * 128 * 128 + (k & 3) * 32, 16), desc_sw128(lb + (k >> 2) * BT * 128 + (k & 3) * 32, 16),
-                         kIdS, 1u);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              mma_f16_ss(s, desc_sw128(qb + (k >> 2) * 128 * 128 + (k & 3) * 32, 16), desc_sw128(hb + (k >> 2) * BT * 128 + (k & 3) * 32, 16),
-                         kIdS, 1u);
-            tc_commit(&sh.sfull[g][buf]);
-          }
-          tc_commit(&sh.kempty[st]);
+        // one buffer of S: the weights of tile t - 1 are used up before S of tile t takes their place
+#pragma unroll 1
+        for (int g = 0; g < C::G && ok; ++g) {
+          if (C::NB == 1 && t > sg.t0) add_values(g, i - 1, t - 1 == sg.t0);
+          if (ok) scores(g);
+          if (C::NB == 2 && t > sg.t0 && ok) add_values(g, i - 1, t - 1 == sg.t0);
         }
-        __syncwarp();
-        if (t > sg.t0) add_values(i - 1, t - 1 == sg.t0);
       }
-      if (ok) add_values(i - 1, sg.t1 - 1 == sg.t0);
+#pragma unroll 1
+      for (int g = 0; g < C::G && ok; ++g) add_values(g, i - 1, sg.t1 - 1 == sg.t0);
     }
     if (lane == 0) tc_commit(&sh.drained);
     __syncwarp();
