@@ -2,14 +2,14 @@
 // drafted tokens (include/bitstack.h, bs_cache_attention; few rows: cache_attention.cu, whose comments state the
 // list of tiles and how it is split).
 //
-// With hundreds of query rows the products bound the time, so they run on tcgen05: an item is one (sequence, head,
-// tile of up to 256 query rows), its context is taken in tiles of 128 tokens (D = 256: 128 rows, 64 tokens), and a
-// tile's packed bytes are expanded once in shared memory for all rows.  Per tile and group of 128 rows
-//     S = Q K^T   (M = 128, N = 128, shared memory operands, fp32 in tensor memory)
-//     P = 2^(S f - m) as fp16, written over S in tensor memory
-//     O += P V    (A from tensor memory, B = V with the dims contiguous)
-// with the maximum and sum of a row in the registers of the thread that owns it.  As in the kernel for few rows the
-// reference m follows the maximum only when a score passes it by 2^8, so O is hardly ever rescaled.
+// With many query rows the products bound the time, so they run on tcgen05: an item is one (sequence, head, tile of
+// 128 query rows), its context is taken in tiles of 128 tokens (D = 256: 64), and a tile's packed bytes are expanded
+// once in shared memory for all rows.  Per tile
+//     S = Q K^T             (Q and S in tensor memory, K in shared memory, fp32 sums)
+//     P = 2^(S f - m)       as fp16, written over S in tensor memory
+//     O += P V              (P and O in tensor memory, V in shared memory with the dims contiguous)
+// with the maximum and sum of a row in registers.  As in the kernel for few rows the reference m follows the maximum
+// only when a score passes it by 8 (weights up to 2^8), so O is hardly ever rescaled.
 //
 // Scores stay exact to fp32: a key is b + s (c - 8); s (c - 8) / 2 has 15 bits, so fp16 parts hi = round(s (c - 8) / 2)
 // and lo = the fma's remainder hold it exactly (halved, as s (c - 8) alone may pass fp16's range), and the b of a group
@@ -18,11 +18,14 @@
 // as the rounding of P does, and the lse, which is fp32, by more than fp32 allows.  Values are rounded to fp16 by
 // one fma.
 //
-// Roles: 4 warps a group own its rows (softmax, output); 8 warps copy packed tiles ahead and expand them; one thread
-// issues all products.  The two groups take turns on the tensor pipe: while one's rows are at their softmax the other's
-// products run (PV of tile t - 1, then S of tile t, group after group).  128 tokens a product (and not 64) because an
-// operand from shared memory is read at 128 bytes a clock: at N = 64 reading Q again for every 64 tokens
-// takes longer than multiplying.
+// Roles: 8 warps own the rows, two threads a row with half a tile's tokens each (softmax, output); one warp walks the list
+// and has the packed tiles copied ahead (one bulk copy a chunk); 8 warps expand them, the keys of tile t + 1 before the
+// values of tile t, whose stage waits for tile t - 1's products; one thread issues all products, S of tile t before O of
+// tile t - 1, so that the tensor pipe works on the next tile while the rows are at this one's softmax.
+// What was measured on the way (2 sequences of 512 new tokens over 4K, 4 heads a key head): two groups of 128 rows with
+// Q in shared memory, 64-token products 141 us, 128-token products 128 us: an operand in shared memory is read at 128
+// bytes a clock, and Q and K together take the products' whole time (or more, at 64 tokens) for it.  Q in tensor memory
+// halves that, and leaves room for two buffers of S with one group.
 //
 // 8 numbers of a word are kept in the order (0, 4, 1, 5, 2, 6, 3, 7) that unpacking gives, in Q and K alike (a sum
 // does not mind), and in V as the order of O's columns, undone where rows are written.
@@ -42,39 +45,38 @@ constexpr float kLag = 8.0f;            // how far scores may pass it
 
 template <int D>
 struct PCfg {
-  static constexpr int G = D == 256 ? 1 : 2;               // groups of 128 rows
-  static constexpr int R = 128 * G;
+  static constexpr int R = 128;                            // query rows of an item
   static constexpr int BT = D == 256 ? 64 : 128;           // tokens of a tile
-  static constexpr int NB = D == 256 ? 2 : 1;              // buffers of S: a single group alternates between two
-  static constexpr int ST = D == 64 ? 2 : 1;               // K and V stages
-  static constexpr int AHEAD = 1;                          // packed tiles requested ahead of the one in use
+  static constexpr int KST = 2, VST = D == 64 ? 2 : 1;     // stages of K and V
   static constexpr int H = D / 64;                         // 128-byte column blocks of a row
   static constexpr int GR = D / 32;
   static constexpr int CHUNKS = BT / kChunkTokens;
   static constexpr int TILE_BYTES = CHUNKS * chunk_bytes(D);
-  static constexpr int XW = 8, XT = XW * 32;               // expanding warps, threads
-  static constexpr int THREADS = G * 128 + XT + 32;
-  static constexpr int O_COL = G * NB * BT;                // tensor memory columns: S first (BT each), then O (D each)
+  static constexpr int RT = 256, XT = 256;                 // threads of the rows, of the expansion
+  static constexpr int HALF_BYTES = TILE_BYTES / 2;        // its keys or its values
+  static constexpr int THREADS = RT + XT + 64;
+  static constexpr int O_COL = 2 * BT, Q_COL = O_COL + D;  // tensor memory columns: S twice, O, Q
   static constexpr uint32_t TMEM = 512;
-  static_assert(O_COL + G * D <= 512, "tensor memory");
+  static_assert(Q_COL + D / 2 <= 512, "tensor memory");
 };
 
 template <int D>
 struct alignas(1024) PShared {
   using C = PCfg<D>;
-  uint8_t q[C::G][C::H][128 * 128];     // 128-byte swizzled rows
-  uint8_t khi[C::ST][C::H][C::BT * 128];
-  uint8_t klo[C::ST][C::H][C::BT * 128];
-  uint8_t v[C::ST][C::H][C::BT * 128];
-  uint8_t qx[C::G][128 * 32];           // the 16 columns of sums and of b: core matrices of 8 rows x 16 bytes
-  uint8_t kx[C::ST][C::BT * 32];
-  uint8_t staging[C::AHEAD + 1][C::TILE_BYTES];
-  uint64_t kfull[C::ST], kempty[C::ST], vfull[C::ST], vempty[C::ST];
-  uint64_t qfull[C::G], sfull[C::G][C::NB], pfull[C::G][C::NB], pvdone[C::G][2], drained;
+  uint8_t khi[C::KST][C::H][C::BT * 128];   // 128-byte swizzled rows
+  uint8_t klo[C::KST][C::H][C::BT * 128];
+  uint8_t v[C::VST][C::H][C::BT * 128];
+  uint8_t qx[128 * 32];                     // the 16 columns of sums and of b: core matrices of 8 rows x 16 bytes
+  uint8_t kx[C::KST][C::BT * 32];
+  uint8_t staging[2][2][C::HALF_BYTES];     // packed keys, packed values: of the tile in use and of the next
+  float half[2][2][128];                    // what a row's two threads tell each other
+  uint64_t kfull[C::KST], kempty[C::KST], vfull[C::VST], vempty[C::VST];
+  uint64_t qfull, sfull[2], pfull[2], pvdone[2], drained;
+  uint64_t cfull[2][2], cempty[2][2];       // staging: [keys, values][slot]
   long long scan_total, wsum[32];
   uint32_t tmem;
   int abort, last[2];
-  int good[8];                          // chunks of tile i % 8 that are in the pool
+  int good[8], live[8];                     // of tile i % 8: the chunks that are in the pool, the tokens of the context
   // then long long prefix[n_seqs + 1]
 };
 
@@ -218,23 +220,27 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
   PShared<D>& sh = *reinterpret_cast<PShared<D>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~static_cast<uintptr_t>(1023));
   long long* prefix = reinterpret_cast<long long*>(&sh + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  constexpr int kRowWarps = 4 * C::G, kMmaWarp = kRowWarps + C::XW, BT = C::BT;
+  constexpr int kRowWarps = C::RT / 32, kCopyWarp = kRowWarps + C::XT / 32, kMmaWarp = kCopyWarp + 1, BT = C::BT;
   const List<D> list{p, prefix};
 
   if (warp == kMmaWarp) tmem_alloc(&sh.tmem, C::TMEM);
   if (tid == 0) {
-    for (int i = 0; i < C::ST; ++i) {
-      mbar_init(&sh.kfull[i], C::XW);
+    for (int i = 0; i < C::KST; ++i) {
+      mbar_init(&sh.kfull[i], C::XT / 32);
       mbar_init(&sh.kempty[i], 1);
-      mbar_init(&sh.vfull[i], C::XW);
+    }
+    for (int i = 0; i < C::VST; ++i) {
+      mbar_init(&sh.vfull[i], C::XT / 32);
       mbar_init(&sh.vempty[i], 1);
     }
-    for (int g = 0; g < C::G; ++g) {
-      mbar_init(&sh.qfull[g], 4);
-      for (int b = 0; b < 2; ++b) mbar_init(&sh.pvdone[g][b], 1);
-      for (int b = 0; b < C::NB; ++b) {
-        mbar_init(&sh.sfull[g][b], 1);
-        mbar_init(&sh.pfull[g][b], 4);
+    mbar_init(&sh.qfull, kRowWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.sfull[i], 1);
+      mbar_init(&sh.pfull[i], kRowWarps);
+      mbar_init(&sh.pvdone[i], 1);
+      for (int kv = 0; kv < 2; ++kv) {
+        mbar_init(&sh.cfull[kv][i], 1);
+        mbar_init(&sh.cempty[kv][i], C::XT / 32);
       }
     }
     mbar_init(&sh.drained, 1);
@@ -242,12 +248,10 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     sh.abort = 0;
     sh.scan_total = 0;
   }
-  // the second half of the extra columns is zero where the first holds all sums (D <= 128)
-  if (D <= 128) {
-    for (int i = tid; i < C::G * 128; i += C::THREADS) sts16(sh.qx[i >> 7] + 128 * 16 + (i & 127) * 16, 0, 0, 0, 0);
-    for (int i = tid; i < C::ST * BT; i += C::THREADS) sts16(sh.kx[i / BT] + BT * 16 + (i % BT) * 16, 0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
+  // extra columns that hold no sum are zero
+  for (int i = tid; i < 256; i += C::THREADS) sts16(sh.qx + i * 16, 0, 0, 0, 0);
+  for (int i = tid; i < C::KST * BT * 2; i += C::THREADS) sts16(sh.kx[0] + i * 16, 0, 0, 0, 0);
+  fence_proxy_async_smem();
   for (int base = 0; base < p.st.n_seqs; base += C::THREADS) {
     const int i = base + tid;
     const long long n = i < p.st.n_seqs ? list.count(i) : 0;
@@ -285,8 +289,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       for (size_t e = tid; e < n; e += C::THREADS) p.lse[at + e] = -INFINITY;
   }
 
-  // CTAs with work: at least four tiles each, as what is split has to be joined
-  const long long n = min(static_cast<long long>(gridDim.x), (T + 3) / 4);
+  // CTAs with work: at least two tiles each, as what is split has to be joined
+  const long long n = min(static_cast<long long>(gridDim.x), (T + 1) / 2);
   const bool works = blockIdx.x < n;
   const long long c0 = works ? T * blockIdx.x / n : 0, c1 = works ? T * (blockIdx.x + 1) / n : 0;
   volatile int* abort = &sh.abort;
@@ -302,26 +306,25 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 
   if (warp < kRowWarps) {
     // ------------------------------------------------------------ rows: softmax and output
-    const int g = warp >> 2, r = (warp & 3) * 32 + lane;        // the thread's group and row in it
+    // Thread (r, hf): row r, tokens hf BT / 2 .. of a tile, output columns hf D / 2 ..
+    const int r = (warp & 3) * 32 + lane, hf = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_at = lanes + C::O_COL + g * D;
+    const uint32_t o_at = lanes + C::O_COL + hf * (D / 2);
+    const int kBar = 3 + (warp & 3);                            // barrier of the two warps of the same rows
     uint32_t i = 0;                                             // tiles so far: phases of all barriers
     bool ok = true;
     for (long long tile = c0; tile < c1 && ok;) {
       const Segment sg = list.at(tile, c1);
       tile = sg.id + sg.t1;
-      const int row = sg.rt * C::R + g * 128 + r, total = sg.rows * p.group;
+      const int row = sg.rt * C::R + r, total = sg.rows * p.group;
       const bool there = row < total;
       const int tok = row / p.group, hq = sg.h * p.group + row % p.group;
       const int pos = there ? sg.start + tok : -1;
       const int low = there ? pos - p.window : -1;              // positions at or below it are hidden
-      // the group's first and last row that exist
-      const int row_a = sg.rt * C::R + g * 128, row_b = min(row_a + 128, total) - 1;
-      const int lowest = row_a < total ? sg.start + row_a / p.group : -1;
-      const int highest = row_a < total ? sg.start + row_b / p.group : -1;
+      const int lowest = sg.start + sg.rt * C::R / p.group, highest = sg.end - 1;
       float f;
       {
-        // the row as fp16, its largest entry in [1, 2), in the operand's layout; sums over groups, halved
+        // the row as fp16, its largest entry in [1, 2), into tensor memory; sums over groups, halved, into qx
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + (sg.row0 + tok) * p.q_tok + static_cast<long long>(hq) * p.q_head;
         auto word = [&](int w) { return there ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0); };
         auto two = [&](uint32_t x) {
@@ -348,14 +351,13 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
         if (p.scale_log2 < 0.0f) scale = -scale;
         if (p.scale_log2 == 0.0f) scale = 0.0f;
-        __half hi[C::GR], lo[C::GR];
-#pragma unroll
-        for (int gr = 0; gr < C::GR; ++gr) {
+#pragma unroll 1
+        for (int gr = hf * (C::GR / 2); gr < (hf + 1) * (C::GR / 2); ++gr) {
           float sum = 0.0f;
+          uint32_t cols[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int w = 4 * gr + k;
-            const uint4 a = word(w);
+            const uint4 a = word(4 * gr + k);
             const uint32_t x[4] = {a.x, a.y, a.z, a.w};
             float y[8];
 #pragma unroll
@@ -367,53 +369,59 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
               y[2 * e] = b.x;
               y[2 * e + 1] = b.y;
             }
-            sts16(sh.q[g][w >> 3] + swz(r, w & 7), h2u(__floats2half2_rn(y[0], y[4])), h2u(__floats2half2_rn(y[1], y[5])),
-                  h2u(__floats2half2_rn(y[2], y[6])), h2u(__floats2half2_rn(y[3], y[7])));
-          }
-          sum *= 0.5f;
-          hi[gr] = __float2half_rn(sum);
-          lo[gr] = __float2half_rn(sum - __half2float(hi[gr]));
-        }
-        // 16 columns: the sums' first parts, then their second (D = 256: 8 and 8; else within the first 8)
-        __half cols[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) cols[e] = e < C::GR ? hi[e % C::GR] : e < 2 * C::GR ? lo[e % C::GR] : __float2half(0.0f);
-        const uint32_t* cw = reinterpret_cast<const uint32_t*>(cols);
-        sts16(sh.qx[g] + r * 16, cw[0], cw[1], cw[2], cw[3]);
-        if (D > 128) sts16(sh.qx[g] + 128 * 16 + r * 16, cw[4], cw[5], cw[6], cw[7]);
+            for (int e = 0; e < 4; ++e) cols[4 * k + e] = h2u(__floats2half2_rn(y[e], y[e + 4]));
+          }
+          tmem_st16(lanes + C::Q_COL + gr * 16, cols);
+          sum *= 0.5f;
+          const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
+          auto put = [&](int col, __half x) {
+            *reinterpret_cast<__half*>(sh.qx + (col >> 3) * (128 * 16) + r * 16 + (col & 7) * 2) = x;
+          };
+          put(gr, hi);
+          put(C::GR + gr, lo);
+        }
+        tc_wait_st();
         fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.qfull[g]);
+        if (lane == 0) mbar_arrive(&sh.qfull);
       }
       float m = kNothing, l = 0.0f;
       for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int buf = i % C::NB;
-        const uint32_t s_at = lanes + (g * C::NB + buf) * BT;
-        ok = wait(&sh.sfull[g][buf], i / C::NB);
-        if (!ok) break;
+        const int buf = i & 1;
+        const uint32_t s_at = lanes + buf * BT + hf * (BT / 2);
+        const int pos0 = sg.first + t * BT + hf * (BT / 2);     // of the thread's first token
+        ok = wait(&sh.sfull[buf], i >> 1) && ok;
         tc_fence_after();
-        const int pos0 = sg.first + t * BT;
-        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 7]);
-        const bool masked = pos0 + BT - 1 > lowest || pos0 <= highest - p.window || good != (1 << C::CHUNKS) - 1;
-        // 32 scores at a time, twice: for the maximum, and for the weights.  Hidden scores become -inf: tokens
+        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 7]) >> (hf * C::CHUNKS / 2) & ((1 << C::CHUNKS / 2) - 1);
+        const bool masked = pos0 + BT / 2 - 1 > lowest || pos0 <= highest - p.window || good != (1 << C::CHUNKS / 2) - 1;
+        // Hidden scores become -inf: tokens
         // behind the row's own, those the window leaves out, chunks outside the pool.
         const int above = pos - pos0, under = low - pos0;
-        auto hide = [&](uint32_t (&x)[32], int c) {
+        uint32_t x[BT / 64][32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j > above || c + j <= under || !((good >> (c / 16 + j / 16)) & 1)) x[j] = 0xff800000u;
-        };
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t x[32];
-#pragma unroll 1
-        for (int c = 0; c < BT; c += 32) {
-          tmem_ld32(s_at + c, x);
-          tc_wait_ld();
-          if (masked) hide(x, c);
+        for (int c = 0; c < BT / 64; ++c) tmem_ld32(s_at + c * 32, x[c]);
+        tc_wait_ld();
+        if (masked) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[j]));
+          for (int c = 0; c < BT / 64; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int k = c * 32 + j;
+              if (k > above || k <= under || !((good >> (k / 16)) & 1)) x[c][j] = 0xff800000u;
+            }
         }
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < BT / 64; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[c][j]));
+        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
+        sh.half[buf][hf][r] = top;
+        ok = !bar_any(kBar, 64, !ok);                           // the two warps of the same rows
+        if (!ok) break;
+        top = fmaxf(top, sh.half[buf][hf ^ 1][r]);
         const bool passed = top > m + kLag;
         if (__any_sync(0xffffffffu, passed)) {
           const float mn = passed ? top : m;
@@ -421,54 +429,54 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           l *= keep;
           m = mn;
           if (t > sg.t0) {                                      // O of this item exists once the tile before is added
-            ok = wait(&sh.pvdone[g][(i - 1) & 1], (i - 1) >> 1);
-            if (!ok) break;
+            ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);   // (a failure is seen at the next barrier)
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              tmem_ld32(o_at + c, x);
+            for (int c = 0; c < D / 2; c += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_at + c, o);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * keep);
-              tmem_st32(o_at + c, x);
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+              tmem_st16(o_at + c, o);
             }
           }
         }
         float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
-        for (int c = 0; c < BT; c += 32) {
-          tmem_ld32(s_at + c, x);
-          tc_wait_ld();
-          if (masked) hide(x, c);
+#pragma unroll
+        for (int c = 0; c < BT / 64; ++c) {
           uint32_t pr[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
-            const float a = ex2(fmaf(__uint_as_float(x[j]), f, -m)), b = ex2(fmaf(__uint_as_float(x[j + 1]), f, -m));
+            const float a = ex2(fmaf(__uint_as_float(x[c][j]), f, -m)), b = ex2(fmaf(__uint_as_float(x[c][j + 1]), f, -m));
             l4[j & 2] += a;
             l4[(j & 2) + 1] += b;
             pr[j / 2] = h2u(__floats2half2_rn(a, b));
           }
-          tmem_st16(s_at + c / 2, pr);                          // over scores that have been read
+          tmem_st16(s_at + c * 16, pr);                         // over scores of this thread
         }
         l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.pfull[g][buf]);
+        if (lane == 0) mbar_arrive(&sh.pfull[buf]);
       }
+      // The segment's O: all of the item, or this CTA's part of it.  (Two barriers for the tiles' ends, as that of tile
+      // i - 1 may or may not have been waited for: the one two tiles before it is over for sure when S of
+      // tile i is there, so a parity never stands for an older phase.)
+      ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1) && ok;
+      sh.half[i & 1][hf][r] = l;                                // read at this parity's barrier below, written next two tiles on
+      ok = !bar_any(kBar, 64, !ok);
       if (!ok) break;
-      // the segment's O: all of the item, or this CTA's part of it
-      // (a barrier for every other tile, as tile i - 1 may or may not be waited for: the tiles two before it are done
-      // for sure when S of tile i is there, so a parity never stands for an older phase)
-      ok = wait(&sh.pvdone[g][(i - 1) & 1], (i - 1) >> 1);
-      if (!ok) break;
+      l += sh.half[i & 1][hf ^ 1][r];
       tc_fence_after();
       const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
       const size_t at = static_cast<size_t>(sg.row0 + tok) * p.q_heads + hq;
-      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R) + g * 128 + r;
+      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R) + r;
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
+      for (int c = 0; c < D / 2; c += 32) {
+        const int col = hf * (D / 2) + c;
         uint32_t o[32];
         tmem_ld32(o_at + c, o);
         tc_wait_ld();
@@ -476,94 +484,47 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           if (there) {
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              float x[8];
+              float y[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(o[8 * w + e]);
-              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(x, inv, p.bf16);
+              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * w + e]);
+              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[col / 8 + w] = out_word(y, inv, p.bf16);
             }
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) part[(c + j) * C::R] = __uint_as_float(o[j]);
+          for (int j = 0; j < 32; ++j) part[(col + j) * C::R] = __uint_as_float(o[j]);
         }
       }
       tc_fence_before();
-      if (whole) {
-        if (there && p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
-      } else {
-        part[D * C::R] = m;
-        part[(D + 1) * C::R] = l;
-      }
-    }
-  } else if (warp < kMmaWarp) {
-    // ------------------------------------------------------------ packed tiles to operands
-    const int d = tid - kRowWarps * 32;                         // 0 .. XT - 1
-    // The next tile to request, and in lane m the table's entry for its chunk m, loaded a tile earlier.
-    long long next = c0;
-    Segment ahead{};
-    int ahead_t = 0, entry = 0;
-    uint32_t n_asked = 0;
-    auto look = [&]() {
-      if (next >= c1) return;
-      if (next == c0 || ahead_t == ahead.t1) {
-        ahead = list.at(next, c1);
-        ahead_t = ahead.t0;
-      }
-      const int pos = ahead.first + ahead_t * BT + lane * kChunkTokens;
-      entry = lane < C::CHUNKS && pos < ahead.end
-                  ? __ldg(p.st.table + static_cast<size_t>(ahead.seq) * p.st.stride + (pos >> p.st.page_shift)) : -1;
-    };
-    auto request = [&]() {
-      if (next < c1) {
-        const int pos = ahead.first + ahead_t * BT + lane * kChunkTokens;
-        const bool wanted = lane < C::CHUNKS && pos < ahead.end;
-        const uint8_t* mine = wanted ? chunk_at(p.st, entry, pos, ahead.h, D) : nullptr;
-        const unsigned there = __ballot_sync(0xffffffffu, mine != nullptr);
-        if (d == 0) sh.good[n_asked & 7] = static_cast<int>(there);
-        if (wanted && mine == nullptr && d < 32) atomicOr(p.st.err, kErrRange);
-        const uint32_t dst = smem_u32(sh.staging[n_asked % (C::AHEAD + 1)]);
-        constexpr int UC = chunk_bytes(D) / 16, UNITS = C::TILE_BYTES / 16;
-#pragma unroll
-        for (int k = 0; k < (UNITS + C::XT - 1) / C::XT; ++k) {
-          const int u = k * C::XT + d, ck = min(u / UC, C::CHUNKS - 1);
-          const unsigned long long base = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), ck);
-          if (UNITS % C::XT != 0 && u >= UNITS) continue;
-          const bool in = base != 0;
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + u * 16),
-                       "l"(in ? reinterpret_cast<const uint8_t*>(base) + (u - ck * UC) * 16 : p.st.pages), "r"(in ? 16 : 0)
-                       : "memory");
+      if (hf == 0) {
+        if (!whole) {
+          part[D * C::R] = m;
+          part[(D + 1) * C::R] = l;
+        } else if (there && p.lse != nullptr) {
+          p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
-        ++next;
-        ++ahead_t;
-        ++n_asked;
-        look();
       }
-      cp_async_commit();
-    };
-    look();
-    for (int k = 0; k < C::AHEAD; ++k) request();
-    uint32_t i = 0;
+      bar_named(kBar, 64);                                      // `half` is free for the next item
+    }
+  } else if (warp < kCopyWarp) {
+    // ------------------------------------------------------------ packed tiles to operands
+    const int d = tid - C::RT;                                  // 0 .. XT - 1
+    const uint32_t tiles = static_cast<uint32_t>(c1 - c0);
     bool ok = true;
-    for (long long tile = c0; tile < c1 && ok;) {
-      const Segment sg = list.at(tile, c1);
-      tile = sg.id + sg.t1;
-      for (int t = sg.t0; t < sg.t1; ++t, ++i) {
-        const int st = i % C::ST;
-        const int pos0 = sg.first + t * BT;
-        cp_async_wait<C::AHEAD - 1>();
-        bar_named(1, C::XT);                                    // the tile is there, and the one before is no longer read
-        request();
-        const uint8_t* tb = sh.staging[i % (C::AHEAD + 1)];
-        if (i >= C::ST) ok = wait(&sh.kempty[st], i / C::ST - 1);
-        ok = !bar_any(2, C::XT, !ok);
+    // K of tile i, then V of tile i - 1
+    for (uint32_t i = 0; i <= tiles && tiles > 0; ++i) {
+      if (i < tiles) {
+        const int st = i % C::KST;
+        ok = wait(&sh.cfull[0][i & 1], i >> 1) && (i < C::KST || wait(&sh.kempty[st], i / C::KST - 1));
         if (!ok) break;
+        const uint8_t* tb = sh.staging[0][i & 1];
         // K: 16 bytes of codes at a time; rows r and r + 4 in neighbouring quarter warps fill all banks
 #pragma unroll
         for (int k = 0; k < BT * (D / 32) / C::XT; ++k) {
           constexpr int UR = D / 32;                            // units of a row
           const int u = k * C::XT + d, q = u / UR, c = u % UR;
           const int row = UR == 4 ? (q & ~7) | ((q & 1) << 2) | ((q >> 1) & 3) : q;
-          const uint8_t* ch = tb + (row >> 4) * chunk_bytes(D);
+          const uint8_t* ch = tb + (row >> 4) * (10 * D);
           const uint4 cw = *reinterpret_cast<const uint4*>(ch + (row & 15) * (D / 2) + c * 16);
           const uint32_t w4[4] = {cw.x, cw.y, cw.z, cw.w};
           const uint32_t* prs = reinterpret_cast<const uint32_t*>(ch + 8 * D + (row & 15) * (D / 8));
@@ -587,7 +548,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           }
         }
         if (d < BT) {                                           // the b of a token's groups, twice
-          const uint32_t* prs = reinterpret_cast<const uint32_t*>(tb + (d >> 4) * chunk_bytes(D) + 8 * D + (d & 15) * (D / 8));
+          const uint32_t* prs = reinterpret_cast<const uint32_t*>(tb + (d >> 4) * (10 * D) + 8 * D + (d & 15) * (D / 8));
           uint32_t b[4];
           if constexpr (D == 64) {
             b[0] = __byte_perm(prs[0], prs[1], 0x7632);
@@ -606,9 +567,15 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.kfull[st]);
-        if (i >= C::ST) ok = wait(&sh.vempty[st], i / C::ST - 1);
-        ok = !bar_any(2, C::XT, !ok);
+        if (lane == 0) mbar_arrive(&sh.cempty[0][i & 1]);
+      }
+      if (i > 0) {
+        const uint32_t j = i - 1;
+        const int vs = j % C::VST;
+        ok = wait(&sh.cfull[1][j & 1], j >> 1) && (j < C::VST || wait(&sh.vempty[vs], j / C::VST - 1));
         if (!ok) break;
+        const uint8_t* tb = sh.staging[1][j & 1];
+        const int good = sh.good[j & 7], live = sh.live[j & 7];
         // V: rows of tokens as they are; tokens behind the item's context become zeros
 #pragma unroll
         for (int k = 0; k < BT * (D / 32) / C::XT; ++k) {
@@ -616,16 +583,16 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           const int u = k * C::XT + d, q = u / UR, c = u % UR;
           const int pr = UR == 4 ? (q & ~15) | ((q & 1) << 3) | ((q >> 1) & 7) : q;   // rows p and p + 8: tokens 2 p, 2 p + 1
           const int row = (pr & ~15) | ((pr & 7) * 2 + ((pr >> 3) & 1));              // the token
-          const uint8_t* ch = tb + (pr >> 4) * chunk_bytes(D) + 10 * D;
+          const uint8_t* ch = tb + (pr >> 4) * (10 * D);
           const uint4 cw = *reinterpret_cast<const uint4*>(ch + (pr & 15) * (D / 2) + c * 16);
           const uint32_t w4[4] = {cw.x, cw.y, cw.z, cw.w};
           const uint32_t* prs = reinterpret_cast<const uint32_t*>(ch + 8 * D + (pr & 15) * (D / 8));
-          const bool live = pos0 + row < sg.end;
+          const bool there = row < live && ((good >> (row >> 4)) & 1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int place = 4 * c + e, w = place / C::H + 8 * (place % C::H);       // C::H = D / 64
             const int gr = w >> 2, pp = (gr & 1) * C::H + (gr >> 1);
-            const uint32_t sb = live ? prs[pp] : 0;
+            const uint32_t sb = there ? prs[pp] : 0;
             const __half2 s2 = __low2half2(u2h(sb)), b2 = __high2half2(u2h(sb));
             uint32_t x4[4];
 #pragma unroll
@@ -635,74 +602,105 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
                                         : __hadd2(u2h(and_or(x, 0x000f000fu, 0x64006400u)), u2h(0xe408e408u));    // - 1032
               x4[n4] = h2u(__hfma2(c2, s2, b2));
             }
-            sts16(sh.v[st][w >> 3] + swz(row, w & 7), x4[0], x4[1], x4[2], x4[3]);
+            sts16(sh.v[vs][w >> 3] + swz(row, w & 7), x4[0], x4[1], x4[2], x4[3]);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.vfull[st]);
+        if (lane == 0) {
+          mbar_arrive(&sh.vfull[vs]);
+          mbar_arrive(&sh.cempty[1][j & 1]);
+        }
       }
     }
-    cp_async_wait<0>();
+  } else if (warp == kCopyWarp) {
+    // ------------------------------------------------------------ packed tiles, ahead of their use
+    uint32_t i = 0;
+    bool ok = true;
+    int entry = 0;                                              // lane m: the table's entry of the next tile's chunk m
+    for (long long tile = c0; tile < c1 && ok;) {
+      const Segment sg = list.at(tile, c1);
+      tile = sg.id + sg.t1;
+      auto look = [&](int t) {
+        const int pos = sg.first + t * BT + lane * kChunkTokens;
+        entry = lane < C::CHUNKS && pos < sg.end
+                    ? __ldg(p.st.table + static_cast<size_t>(sg.seq) * p.st.stride + (pos >> p.st.page_shift)) : -1;
+      };
+      look(sg.t0);
+      for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
+        const int pos0 = sg.first + t * BT, pos = pos0 + lane * kChunkTokens;
+        const bool wanted = lane < C::CHUNKS && pos < sg.end;
+        const uint8_t* src = wanted ? chunk_at(p.st, entry, pos, sg.h, D) : nullptr;
+        if (t + 1 < sg.t1) look(t + 1);
+        if (wanted && src == nullptr) atomicOr(p.st.err, kErrRange);
+        const unsigned there = __ballot_sync(0xffffffffu, src != nullptr);
+        if (lane == 0) {
+          sh.good[i & 7] = static_cast<int>(there);
+          sh.live[i & 7] = sg.end - pos0;
+        }
+#pragma unroll
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          if (i >= 2) ok = wait(&sh.cempty[kv][i & 1], (i >> 1) - 1);
+          if (!ok) break;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.cfull[kv][i & 1], __popc(there) * 10 * D);
+          __syncwarp();
+          if (src != nullptr)
+            bulk_g2s(sh.staging[kv][i & 1] + lane * 10 * D, src + kv * 10 * D, 10 * D, &sh.cfull[kv][i & 1]);
+          __syncwarp();
+        }
+      }
+    }
+    // what was asked for last may still be on its way after a failure
+    for (uint32_t back = 1; back <= 2 && back <= i && !ok; ++back)
+      for (int kv = 0; kv < 2; ++kv) mbar_wait(&sh.cfull[kv][(i - back) & 1], ((i - back) >> 1) & 1, globaltimer_ns() + p.timeout_ns, nullptr);
   } else {
     // ------------------------------------------------------------ products
     constexpr uint32_t kIdS = make_idesc(1u, 0u, 0u, 128u, BT);
     constexpr uint32_t kIdO = make_idesc(1u, 0u, 0u, 128u, D) | 1u << 16;   // B with N contiguous
     uint32_t i = 0, segs = 0;
     bool ok = true;
-    auto add_values = [&](int g, uint32_t j, bool begin) {      // O += P V of tile j
-      const int st = j % C::ST, buf = j % C::NB;
-      if (g == 0) ok = wait(&sh.vfull[st], j / C::ST);
-      if (ok) ok = wait(&sh.pfull[g][buf], j / C::NB);
+    auto add_values = [&](uint32_t j, bool begin) {             // O += P V of tile j
+      const int st = j % C::VST, buf = j & 1;
+      ok = wait(&sh.vfull[st], j / C::VST) && wait(&sh.pfull[buf], j >> 1);
       if (!ok) return;
       tc_fence_after();
       if (lane == 0) {
-        const uint32_t a = tmem + (g * C::NB + buf) * BT, o = tmem + C::O_COL + g * D;
-        const uint32_t vb = desc_lo(smem_u32(sh.v[st][0]), BT * 128);
+        const uint32_t a = tmem + buf * BT, o = tmem + C::O_COL, vb = desc_lo(smem_u32(sh.v[st][0]), BT * 128);
+        // the weights of a tile's halves stand at the begin of their halves of S
 #pragma unroll
-        for (int k = 0; k < BT / 16; ++k) mma_ts<kSw128>(o, a + k * 8, vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
-        tc_commit(&sh.pvdone[g][j & 1]);
-        if (g == C::G - 1) tc_commit(&sh.vempty[st]);
-      }
-      __syncwarp();
-    };
-    auto scores = [&](int g) {                                  // S of tile i
-      const int st = i % C::ST, buf = i % C::NB;
-      if (g == 0) ok = wait(&sh.kfull[st], i / C::ST);
-      if (!ok) return;
-      tc_fence_after();
-      if (lane == 0) {
-        const uint32_t hb = desc_lo(smem_u32(sh.khi[st][0]), 16), lb = desc_lo(smem_u32(sh.klo[st][0]), 16);
-        const uint32_t s = tmem + (g * C::NB + buf) * BT, qb = desc_lo(smem_u32(sh.q[g][0]), 16);
-        // smallest parts first: b sum q, then the remainders, then the rest
-        mma_ss<kPlain>(s, desc_lo(smem_u32(sh.qx[g]), 128 * 16), desc_lo(smem_u32(sh.kx[st]), BT * 16), kIdS, 0u);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss<kSw128>(s, qb + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4), lb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_ss<kSw128>(s, qb + (((k >> 2) * 128 * 128 + (k & 3) * 32) >> 4), hb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
-        tc_commit(&sh.sfull[g][buf]);
-        if (g == C::G - 1) tc_commit(&sh.kempty[st]);
+        for (int k = 0; k < BT / 16; ++k)
+          mma_ts<kSw128>(o, a + (k < BT / 32 ? k * 8 : BT / 2 + (k - BT / 32) * 8), vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
+        tc_commit(&sh.pvdone[buf]);
+        tc_commit(&sh.vempty[st]);
       }
       __syncwarp();
     };
     for (long long tile = c0; tile < c1 && ok; ++segs) {
       const Segment sg = list.at(tile, c1);
       tile = sg.id + sg.t1;
-      for (int g = 0; g < C::G && ok; ++g) ok = wait(&sh.qfull[g], segs);
+      ok = wait(&sh.qfull, segs);
 #pragma unroll 1
       for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {
-        // one buffer of S: the weights of tile t - 1 are used up before S of tile t takes their place
-#pragma unroll 1
-        for (int g = 0; g < C::G && ok; ++g) {
-          if (C::NB == 1 && t > sg.t0) add_values(g, i - 1, t - 1 == sg.t0);
-          if (ok) scores(g);
-          if (C::NB == 2 && t > sg.t0 && ok) add_values(g, i - 1, t - 1 == sg.t0);
+        const int st = i % C::KST, buf = i & 1;
+        ok = wait(&sh.kfull[st], i / C::KST);
+        if (!ok) break;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint32_t hb = desc_lo(smem_u32(sh.khi[st][0]), 16), lb = desc_lo(smem_u32(sh.klo[st][0]), 16);
+          const uint32_t s = tmem + buf * BT, q = tmem + C::Q_COL;
+          // smallest parts first: b sum q, then the remainders, then the rest
+          mma_ss<kPlain>(s, desc_lo(smem_u32(sh.qx), 128 * 16), desc_lo(smem_u32(sh.kx[st]), BT * 16), kIdS, 0u);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) mma_ts<kSw128>(s, q + k * 8, lb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k) mma_ts<kSw128>(s, q + k * 8, hb + (((k >> 2) * BT * 128 + (k & 3) * 32) >> 4), kIdS, 1u);
+          tc_commit(&sh.sfull[buf]);
+          tc_commit(&sh.kempty[st]);
         }
+        __syncwarp();
+        if (t > sg.t0) add_values(i - 1, t - 1 == sg.t0);
       }
-#pragma unroll 1
-      for (int g = 0; g < C::G && ok; ++g) add_values(g, i - 1, sg.t1 - 1 == sg.t0);
+      if (ok) add_values(i - 1, sg.t1 - 1 == sg.t0);
     }
     if (lane == 0) tc_commit(&sh.drained);
     __syncwarp();
@@ -736,36 +734,42 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     if (!sh.last[it]) continue;
     const Segment sg = list.at(it == 0 ? c0 : c1 - 1, c1);
     const int f0 = cta_of(sg.id), parts = cta_of(sg.id + sg.tiles - 1) - f0 + 1;
-    if (tid >= C::R) continue;
-    const int row = sg.rt * C::R + tid;
+    // four threads a row, a quarter of the columns each
+    const int r = tid & 127, quarter = tid >> 7;
+    if (quarter >= 4) continue;
+    const int row = sg.rt * C::R + r;
     if (row >= sg.rows * p.group) continue;
-    auto part_of = [&](int x) { return p.part + static_cast<size_t>((f0 + x) * 2 + (x == 0 ? 1 : 0)) * ((D + 2) * C::R) + tid; };
+    const float* base = p.part + static_cast<size_t>(f0) * 2 * ((D + 2) * C::R) + r;
+    auto part_of = [&](int x) { return base + static_cast<size_t>(2 * x + (x == 0 ? 1 : 0)) * ((D + 2) * C::R); };
     float m = kNothing, l = 0.0f;
+#pragma unroll 4
     for (int x = 0; x < parts; ++x) m = fmaxf(m, part_of(x)[D * C::R]);
+#pragma unroll 4
     for (int x = 0; x < parts; ++x) l = fmaf(ex2(part_of(x)[D * C::R] - m), part_of(x)[(D + 1) * C::R], l);
     const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
     const size_t at = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
+    constexpr int kCols = D / 4 < 32 ? D / 4 : 32;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      float o[32];
+    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += kCols) {
+      float o[kCols];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = 0.0f;
-#pragma unroll 1
+      for (int j = 0; j < kCols; ++j) o[j] = 0.0f;
+#pragma unroll 2
       for (int x = 0; x < parts; ++x) {
         const float* f = part_of(x);
         const float w = ex2(f[D * C::R] - m);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = fmaf(w, f[(c + j) * C::R], o[j]);
+        for (int j = 0; j < kCols; ++j) o[j] = fmaf(w, f[(c + j) * C::R], o[j]);
       }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        float x[8];
+      for (int w = 0; w < kCols / 8; ++w) {
+        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = o[8 * w + e];
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(x, inv, p.bf16);
+        for (int e = 0; e < 8; ++e) y[e] = o[8 * w + e];
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(y, inv, p.bf16);
       }
     }
-    if (p.lse != nullptr) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (p.lse != nullptr && quarter == 0) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
 
@@ -794,7 +798,7 @@ size_t cache_prefill_smem(int dim, int n_seqs) {
   const size_t fixed = dim == 64 ? sizeof(PShared<64>) : dim == 128 ? sizeof(PShared<128>) : sizeof(PShared<256>);
   return fixed + 1024 + (static_cast<size_t>(n_seqs) + 1) * 8;
 }
-size_t cache_prefill_part_floats(int dim) { return static_cast<size_t>(dim + 2) * (dim == 256 ? PCfg<256>::R : PCfg<128>::R); }
+size_t cache_prefill_part_floats(int dim) { return static_cast<size_t>(dim + 2) * PCfg<128>::R; }
 cudaError_t launch_cache_prefill(const CacheAttnParams& p, int dim, cudaStream_t stream) {
   return dim == 64 ? launch_as<64>(p, stream) : dim == 128 ? launch_as<128>(p, stream) : launch_as<256>(p, stream);
 }
