@@ -304,7 +304,10 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     return ok;
   };
 
+  // Rows hold a tile's scores in registers, the expansion needs fewer than the launch gives everyone: 8 warps take
+  // 24 registers a thread from 8 others.
   if (warp < kRowWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ------------------------------------------------------------ rows: softmax and output
     // Thread (r, hf): row r, tokens hf BT / 2 .. of a tile, output columns hf D / 2 ..
     const int r = (warp & 3) * 32 + lane, hf = warp >> 2;
@@ -324,23 +327,30 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       const int lowest = sg.start + sg.rt * C::R / p.group, highest = sg.end - 1;
       float f;
       {
-        // the row as fp16, its largest entry in [1, 2), into tensor memory; sums over groups, halved, into qx
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + (sg.row0 + tok) * p.q_tok + static_cast<long long>(hq) * p.q_head;
-        auto word = [&](int w) { return there ? __ldg(reinterpret_cast<const uint4*>(src) + w) : make_uint4(0, 0, 0, 0); };
+        // the row as fp16, its largest entry in [1, 2), into tensor memory; sums over groups, halved, into qx.  A
+        // thread takes half of the row, all loads at once.
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (sg.row0 + tok) * p.q_tok +
+                                                          static_cast<long long>(hq) * p.q_head) + hf * (D / 16);
+        uint4 raw[D / 16];
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) raw[w] = there ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
         auto two = [&](uint32_t x) {
           return p.bf16 ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)) : __half22float2(u2h(x));
         };
         uint32_t top = 0;
-#pragma unroll 4
-        for (int w = 0; w < D / 8; ++w) {
-          const uint4 a = word(w);
-          const uint32_t x[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int w = 0; w < D / 16; ++w) {
+          const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 v = two(x[e]);
             top = max(top, max(__float_as_uint(v.x) & 0x7f800000u, __float_as_uint(v.y) & 0x7f800000u));
           }
         }
+        sh.half[0][hf][r] = __uint_as_float(top);
+        bar_named(kBar, 64);
+        top = max(top, __float_as_uint(sh.half[0][hf ^ 1][r]));
+        bar_named(kBar, 64);                                    // `half` is free for the tiles
         const int ex = static_cast<int>(top >> 23);
         const int up = min(max(254 - ex, 1), 254);
         float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
@@ -351,13 +361,14 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
         if (p.scale_log2 < 0.0f) scale = -scale;
         if (p.scale_log2 == 0.0f) scale = 0.0f;
-#pragma unroll 1
-        for (int gr = hf * (C::GR / 2); gr < (hf + 1) * (C::GR / 2); ++gr) {
+#pragma unroll
+        for (int g = 0; g < C::GR / 2; ++g) {
+          const int gr = hf * (C::GR / 2) + g;
           float sum = 0.0f;
           uint32_t cols[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 a = word(4 * gr + k);
+            const uint4 a = raw[4 * g + k];
             const uint32_t x[4] = {a.x, a.y, a.z, a.w};
             float y[8];
 #pragma unroll
@@ -418,13 +429,14 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 #pragma unroll
           for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[c][j]));
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-        sh.half[buf][hf][r] = top;
-        ok = !bar_any(kBar, 64, !ok);                           // the two warps of the same rows
-        if (!ok) break;
-        top = fmaxf(top, sh.half[buf][hf ^ 1][r]);
-        const bool passed = top > m + kLag;
-        if (__any_sync(0xffffffffu, passed)) {
-          const float mn = passed ? top : m;
+        // The two warps of the same rows go on together when none of their scores passes the reference; else they
+        // tell each other the rows' maxima.
+        if (bar_any(kBar, 64, top > m + kLag || !ok)) {
+          sh.half[buf][hf][r] = top;
+          ok = !bar_any(kBar, 64, !ok);
+          if (!ok) break;
+          top = fmaxf(top, sh.half[buf][hf ^ 1][r]);
+          const float mn = top > m + kLag ? top : m;
           const float keep = ex2(m - mn);
           l *= keep;
           m = mn;
@@ -506,7 +518,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       }
       bar_named(kBar, 64);                                      // `half` is free for the next item
     }
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");       // all as launched for the code below
   } else if (warp < kCopyWarp) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ------------------------------------------------------------ packed tiles to operands
     const int d = tid - C::RT;                                  // 0 .. XT - 1
     const uint32_t tiles = static_cast<uint32_t>(c1 - c0);
@@ -613,6 +627,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
       }
     }
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ packed tiles, ahead of their use
     uint32_t i = 0;
