@@ -43,6 +43,15 @@ namespace {
 constexpr float kNothing = -3.0e38f;    // the reference before any score
 constexpr float kLag = 8.0f;            // how far scores may pass it
 
+// A run of tiles of one item: tiles t0 .. t1 - 1 of `tiles`.
+struct Segment {
+  long long id;                         // number of the item's first tile
+  int seq, row0, rows, start;           // the sequence
+  int rt, h, first, tiles;              // the item: its row tile, head, first position and tiles
+  int t0, t1;
+  int end;                              // positions its last row sees
+};
+
 template <int D>
 struct PCfg {
   static constexpr int R = 128;                            // query rows of an item
@@ -73,20 +82,14 @@ struct alignas(1024) PShared {
   uint64_t kfull[C::KST], kempty[C::KST], vfull[C::VST], vempty[C::VST];
   uint64_t qfull, sfull[2], pfull[2], pvdone[2], drained;
   uint64_t cfull[2][2], cempty[2][2];       // staging: [keys, values][slot]
+  uint64_t pair[4];                         // the two warps of the same rows meet
+  int say[2][8];                            // and what they have to say then
+  Segment ends[2];                          // the first and the last one of this CTA
   long long scan_total, wsum[32];
   uint32_t tmem;
   int abort, last[2];
   int good[8], live[8];                     // of tile i % 8: the chunks that are in the pool, the tokens of the context
   // then long long prefix[n_seqs + 1]
-};
-
-// A run of tiles of one item: tiles t0 .. t1 - 1 of `tiles`.
-struct Segment {
-  long long id;                         // number of the item's first tile
-  int seq, row0, rows, start;           // the sequence
-  int rt, h, first, tiles;              // the item: its row tile, head, first position and tiles
-  int t0, t1;
-  int end;                              // positions its last row sees
 };
 
 template <int D>
@@ -95,6 +98,7 @@ struct List {
   const CacheAttnParams& p;
   const long long* prefix;
 
+  __device__ int row_tiles(const SeqSpan& s) const { return (s.rows * p.group + C::R - 1) / C::R; }
   // First position, positions seen and tiles of row tile rt of a sequence.
   __device__ void item(const SeqSpan& s, int rt, int& first, int& end, int& tiles) const {
     const int total = s.rows * p.group;
@@ -103,20 +107,24 @@ struct List {
     first = lowest >= p.window ? (lowest - p.window + 1) / kChunkTokens * kChunkTokens : 0;
     tiles = (end - first + C::BT - 1) / C::BT;
   }
-  __device__ long long count(int i) const {
+  // Tiles of row tiles rt0, rt0 + step, ... of sequence i, for all heads.
+  __device__ long long count(int i, int rt0, int step) const {
     const SeqSpan s = seq_span(p.st, i);
     if (!s.live) return 0;
-    const int rts = (s.rows * p.group + C::R - 1) / C::R;
+    const int rts = row_tiles(s);
     long long n = 0;
-    for (int rt = 0; rt < rts; ++rt) {
+    for (int rt = rt0; rt < rts; rt += step) {
       int first, end, tiles;
       item(s, rt, first, end, tiles);
       n += tiles;
     }
     return n * p.st.heads;
   }
-  // The segment that begins at `tile` and goes no further than `stop`.
-  __device__ Segment at(long long tile, long long stop) const {
+  __device__ void cut(Segment& g, long long stop) const {
+    g.t1 = static_cast<int>(min(static_cast<long long>(g.tiles), stop - g.id));
+  }
+  // The segment that begins at `tile` and goes no further than `stop`.  For whole warps: 32 row tiles at a time.
+  __device__ Segment at(long long tile, long long stop, int lane) const {
     int lo = 0, hi = p.st.n_seqs - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) / 2;
@@ -124,23 +132,53 @@ struct List {
       else hi = mid - 1;
     }
     const SeqSpan s = seq_span(p.st, lo);
+    const int rts = row_tiles(s);
     Segment g;
     g.seq = lo;
     g.row0 = s.row0;
     g.rows = s.rows;
     g.start = s.start;
     long long off = tile - prefix[lo];
-    g.rt = 0;
-    item(s, 0, g.first, g.end, g.tiles);
-    while (off >= static_cast<long long>(g.tiles) * p.st.heads) {
-      off -= static_cast<long long>(g.tiles) * p.st.heads;
-      item(s, ++g.rt, g.first, g.end, g.tiles);
+    for (int base = 0;; base += 32) {
+      int first = 0, end = 0, tiles = 0;
+      if (base + lane < rts) item(s, base + lane, first, end, tiles);
+      long long upto = static_cast<long long>(tiles) * p.st.heads;   // tiles up to and with this lane's row tile
+#pragma unroll
+      for (int o = 1; o < 32; o *= 2) {
+        const long long v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, upto > off);
+      if (behind == 0 && base + 32 < rts) {
+        off -= __shfl_sync(0xffffffffu, upto, 31);
+        continue;
+      }
+      const int at = __ffs(behind) - 1;
+      g.rt = base + at;
+      g.first = __shfl_sync(0xffffffffu, first, at);
+      g.end = __shfl_sync(0xffffffffu, end, at);
+      g.tiles = __shfl_sync(0xffffffffu, tiles, at);
+      off -= __shfl_sync(0xffffffffu, upto, at) - static_cast<long long>(g.tiles) * p.st.heads;
+      break;
     }
     g.h = static_cast<int>(off / g.tiles);
     g.t0 = static_cast<int>(off % g.tiles);
     g.id = tile - g.t0;
-    g.t1 = static_cast<int>(min(static_cast<long long>(g.tiles), stop - g.id));
+    cut(g, stop);
     return g;
+  }
+  // The one behind it, which begins an item.
+  __device__ void next(Segment& g, long long stop, int lane) const {
+    const long long tile = g.id + g.tiles;
+    if (tile >= stop) return;
+    if (g.h + 1 < p.st.heads) {
+      ++g.h;
+      g.id = tile;
+      g.t0 = 0;
+      cut(g, stop);
+    } else {
+      g = at(tile, stop, lane);
+    }
   }
 };
 
@@ -243,6 +281,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         mbar_init(&sh.cempty[kv][i], C::XT / 32);
       }
     }
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.pair[i], 2);
     mbar_init(&sh.drained, 1);
     fence_barrier_init();
     sh.abort = 0;
@@ -252,9 +291,22 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
   for (int i = tid; i < 256; i += C::THREADS) sts16(sh.qx + i * 16, 0, 0, 0, 0);
   for (int i = tid; i < C::KST * BT * 2; i += C::THREADS) sts16(sh.kx[0] + i * 16, 0, 0, 0, 0);
   fence_proxy_async_smem();
+  // Tiles of every sequence: a thread counts a sequence's, or a warp where a sequence may have many row tiles; then
+  // their prefix sums.
+  if (static_cast<long long>(p.st.max_new) * p.group > 4 * C::R) {
+    for (int i = warp; i < p.st.n_seqs; i += C::THREADS / 32) {
+      long long n = list.count(i, lane, 32);
+#pragma unroll
+      for (int o = 16; o > 0; o /= 2) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0) prefix[i] = n;
+    }
+  } else {
+    for (int i = tid; i < p.st.n_seqs; i += C::THREADS) prefix[i] = list.count(i, 0, 1);
+  }
+  __syncthreads();
   for (int base = 0; base < p.st.n_seqs; base += C::THREADS) {
     const int i = base + tid;
-    const long long n = i < p.st.n_seqs ? list.count(i) : 0;
+    const long long n = i < p.st.n_seqs ? prefix[i] : 0;
     long long inc = n;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -304,20 +356,33 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     return ok;
   };
 
-  // Rows hold a tile's scores in registers, the expansion needs fewer than the launch gives everyone: 8 warps take
-  // 24 registers a thread from 8 others.
   if (warp < kRowWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;");
     // ------------------------------------------------------------ rows: softmax and output
     // Thread (r, hf): row r, tokens hf BT / 2 .. of a tile, output columns hf D / 2 ..
     const int r = (warp & 3) * 32 + lane, hf = warp >> 2;
     const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t o_at = lanes + C::O_COL + hf * (D / 2);
-    const int kBar = 3 + (warp & 3);                            // barrier of the two warps of the same rows
     uint32_t i = 0;                                             // tiles so far: phases of all barriers
     bool ok = true;
-    for (long long tile = c0; tile < c1 && ok;) {
-      const Segment sg = list.at(tile, c1);
+    // The two warps of the same rows meet: what either wrote to shared memory before is there for the other, and either
+    // knows whether one of them said so, or gave up (then both do).
+    uint32_t met = 0;
+    auto meet = [&](bool said) {
+      said = __any_sync(0xffffffffu, said);
+      if (lane == 0) {
+        *reinterpret_cast<volatile int*>(&sh.say[met & 1][warp]) = (said ? 1 : 0) | (ok ? 0 : 2);
+        mbar_arrive(&sh.pair[warp & 3]);
+      }
+      __syncwarp();
+      ok = wait(&sh.pair[warp & 3], met) && ok;
+      const int other = *reinterpret_cast<volatile int*>(&sh.say[met & 1][warp ^ 4]);
+      if (other & 2) ok = false;
+      ++met;
+      return said || (other & 1) != 0;
+    };
+    Segment sg{};
+    if (works) sg = list.at(c0, c1, lane);
+    for (long long tile = c0; tile < c1 && ok; list.next(sg, c1, lane)) {
       tile = sg.id + sg.t1;
       const int row = sg.rt * C::R + r, total = sg.rows * p.group;
       const bool there = row < total;
@@ -348,9 +413,10 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           }
         }
         sh.half[0][hf][r] = __uint_as_float(top);
-        bar_named(kBar, 64);
+        __syncwarp();
+        meet(false);
         top = max(top, __float_as_uint(sh.half[0][hf ^ 1][r]));
-        bar_named(kBar, 64);                                    // `half` is free for the tiles
+        meet(false);                                            // `half` is free for the tiles
         const int ex = static_cast<int>(top >> 23);
         const int up = min(max(254 - ex, 1), 254);
         float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
@@ -431,9 +497,12 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
         // The two warps of the same rows go on together when none of their scores passes the reference; else they
         // tell each other the rows' maxima.
-        if (bar_any(kBar, 64, top > m + kLag || !ok)) {
+        const bool passed = meet(top > m + kLag);
+        if (!ok) break;
+        if (passed) {
           sh.half[buf][hf][r] = top;
-          ok = !bar_any(kBar, 64, !ok);
+          __syncwarp();
+          meet(false);
           if (!ok) break;
           top = fmaxf(top, sh.half[buf][hf ^ 1][r]);
           const float mn = top > m + kLag ? top : m;
@@ -478,7 +547,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       // tile i is there, so a parity never stands for an older phase.)
       ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1) && ok;
       sh.half[i & 1][hf][r] = l;                                // read at this parity's barrier below, written next two tiles on
-      ok = !bar_any(kBar, 64, !ok);
+      __syncwarp();
+      meet(false);
       if (!ok) break;
       l += sh.half[i & 1][hf ^ 1][r];
       tc_fence_after();
@@ -516,11 +586,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
         }
       }
-      bar_named(kBar, 64);                                      // `half` is free for the next item
+      meet(false);                                              // `half` is free for the next item
     }
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");       // all as launched for the code below
   } else if (warp < kCopyWarp) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     // ------------------------------------------------------------ packed tiles to operands
     const int d = tid - C::RT;                                  // 0 .. XT - 1
     const uint32_t tiles = static_cast<uint32_t>(c1 - c0);
@@ -627,15 +695,17 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
       }
     }
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 96;");
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ packed tiles, ahead of their use
     uint32_t i = 0;
     bool ok = true;
     int entry = 0;                                              // lane m: the table's entry of the next tile's chunk m
-    for (long long tile = c0; tile < c1 && ok;) {
-      const Segment sg = list.at(tile, c1);
+    Segment sg{};
+    if (works) sg = list.at(c0, c1, lane);
+    if (lane == 0) sh.ends[0] = sg;
+    for (long long tile = c0; tile < c1 && ok; list.next(sg, c1, lane)) {
       tile = sg.id + sg.t1;
+      if (lane == 0) sh.ends[1] = sg;
       auto look = [&](int t) {
         const int pos = sg.first + t * BT + lane * kChunkTokens;
         entry = lane < C::CHUNKS && pos < sg.end
@@ -690,8 +760,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       }
       __syncwarp();
     };
-    for (long long tile = c0; tile < c1 && ok; ++segs) {
-      const Segment sg = list.at(tile, c1);
+    Segment sg{};
+    if (works) sg = list.at(c0, c1, lane);
+    for (long long tile = c0; tile < c1 && ok; ++segs, list.next(sg, c1, lane)) {
       tile = sg.id + sg.t1;
       ok = wait(&sh.qfull, segs);
 #pragma unroll 1
@@ -732,7 +803,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
   auto cta_of = [&](long long x) { return static_cast<int>(((x + 1) * n - 1) / T); };
   if (tid < 2) {
     sh.last[tid] = 0;
-    const Segment sg = list.at(tid == 0 ? c0 : c1 - 1, c1);
+    const Segment sg = sh.ends[tid];
     // tid 0: the item at the range's begin, if it began before; tid 1: the one at its end, if it began here and goes on
     const bool mine = tid == 0 ? sg.id < c0 : sg.id >= c0 && sg.id + sg.tiles > c1;
     if (mine) {
@@ -747,7 +818,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 #pragma unroll 1
   for (int it = 0; it < 2; ++it) {
     if (!sh.last[it]) continue;
-    const Segment sg = list.at(it == 0 ? c0 : c1 - 1, c1);
+    const Segment sg = sh.ends[it];
     const int f0 = cta_of(sg.id), parts = cta_of(sg.id + sg.tiles - 1) - f0 + 1;
     // four threads a row, a quarter of the columns each
     const int r = tid & 127, quarter = tid >> 7;
