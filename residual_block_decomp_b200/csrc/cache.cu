@@ -15,6 +15,7 @@
 #include <cuda_fp16.h>
 
 #include "cache.h"
+#include "ptx.cuh"
 
 namespace bs {
 namespace {
@@ -117,6 +118,8 @@ template <int D, typename T, int STEPS>
 __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_constant__ CacheCopyParams p) {
   constexpr int LR = D / 8;                      // lanes of a row
   constexpr int HB = STEPS * 16 / LR;            // heads of a warp's step run
+  griddep_launch_dependents();
+  griddep_wait();
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
   const SeqSpan s = seq_span(p.st, seq);
   if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
@@ -227,6 +230,8 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
   constexpr int UR = D / 32;                     // 16-byte units of a row of codes
   constexpr int N = 16 * UR / 32;                // units of a lane: keys, and as many of values
   constexpr int GR = D / 32, J = D / 64;
+  griddep_launch_dependents();
+  griddep_wait();
   const int seq = blockIdx.y, lane = threadIdx.x & 31;
   const SeqSpan s = seq_span(p.st, seq);
   if (s.bad && blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.st.err, kErrRange);
@@ -257,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         code[kv][i] = __ldg(reinterpret_cast<const uint4*>(base + u * 16));
         const uint8_t* pr = base + 8 * D + row * (D / 8);
         if (kv ? J == 4 : GR >= 4) {             // four consecutive pairs
-          pair[kv][i] = __ldg(reinterpret_cast<const uint4*>(pr + (kv ? c / 4 : c % (GR / 4)) * 16));
+          pair[kv][i] = __ldg(reinterpret_cast<const uint4*>(pr + (kv ? c / 4 : c % (GR < 4 ? 1 : GR / 4)) * 16));
         } else if (kv ? J == 2 : true) {         // two, for words 0, 1 and 2, 3
           const uint2 two = __ldg(reinterpret_cast<const uint2*>(pr + (kv ? c / 2 * 8 : 0)));
           pair[kv][i] = make_uint4(two.x, two.y, two.x, two.y);
@@ -298,8 +303,8 @@ long long longest(const StepParams& s) { return s.max_new < s.n_tokens ? s.max_n
 template <int D, typename T, int STEPS>
 cudaError_t append_steps(const CacheCopyParams& p, cudaStream_t stream) {
   constexpr int HB = STEPS * 16 / (D / 8);
-  cache_append_kernel<D, T, STEPS><<<copy_grid(p.st, longest(p.st) * ((p.st.heads + HB - 1) / HB)), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(cache_append_kernel<D, T, STEPS>, copy_grid(p.st, longest(p.st) * ((p.st.heads + HB - 1) / HB)),
+                        kThreads, 0, stream, p);
 }
 // Four steps of loads in flight a lane where there is work for all SMs' warps, the fewest otherwise.
 template <int D, typename T>
@@ -310,8 +315,8 @@ cudaError_t append_as(const CacheCopyParams& p, cudaStream_t stream) {
 template <int D, typename T>
 cudaError_t read_as(const CacheCopyParams& p, cudaStream_t stream) {
   // a sequence of n positions touches at most n / 16 + 2 chunks
-  cache_read_kernel<D, T><<<copy_grid(p.st, (longest(p.st) / kChunkTokens + 2) * p.st.heads), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(cache_read_kernel<D, T>, copy_grid(p.st, (longest(p.st) / kChunkTokens + 2) * p.st.heads), kThreads,
+                        0, stream, p);
 }
 template <int D>
 cudaError_t append_dim(const CacheCopyParams& p, int dtype, cudaStream_t stream) {

@@ -106,6 +106,23 @@ struct CacheCopyParams {
 cudaError_t launch_cache_append(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);
 
+// Launches the cache's kernels with programmatic dependent launch: a kernel's blocks may be set up while the kernel ahead
+// on the stream ends; each waits for it (griddepcontrol.wait) before it touches device memory.
+template <typename P>
+cudaError_t launch_chained(void (*kernel)(P), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream, const P& p) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
 }  // namespace bs
 
 // The handle.  Host memory only.

@@ -141,7 +141,7 @@ struct Shared {
   using C = Cfg<D, NT>;
   uint8_t stage[C::NW][C::ST][kTileBytes5k];
   FragMeta meta[2 * C::NW];
-  int scan[32];
+  long long wsum[32];
   int last[2];            // slot of a shared item whose parts this CTA adds up; -1: none
   long long scan_total;
   // then long long prefix[n_seqs + 1]
@@ -649,39 +649,62 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const Worker<D, NT> wk{p, prefix, lane};
 
-  // tile counts of all sequences, prefix-summed
-  if (tid == 0) sh.scan_total = 0;
-  for (int base = 0; base < p.st.n_seqs; base += C::NW * 32) {
-    const int i = base + tid;
-    long long n = 0;
-    if (i < p.st.n_seqs) {
-      Cursor c;
-      wk.seq(c, i);
-      n = static_cast<long long>(c.tiles) * c.rts * p.st.heads;
-    }
-    long long inc = n;
+  griddep_launch_dependents();
+  griddep_wait();
+  // Tile counts of all sequences, prefix-summed: by every warp for itself up to 32 sequences (the values they write are
+  // the same), by the CTA beyond.
+  if (lane < 2) sh.meta[2 * warp + lane].id = -1;
+  long long T = 0;
+  auto tiles_of = [&](int i) -> long long {
+    if (i >= p.st.n_seqs) return 0;
+    Cursor c;
+    wk.seq(c, i);
+    return static_cast<long long>(c.tiles) * c.rts * p.st.heads;
+  };
+  auto scan = [&](long long v) {
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
-      const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
+      const long long u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
     }
-    long long* wsum = reinterpret_cast<long long*>(sh.meta);   // not in use yet
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    long long before = sh.scan_total;
-    for (int w = 0; w < warp; ++w) before += wsum[w];
-    if (i < p.st.n_seqs) prefix[i] = before + inc - n;
-    __syncthreads();
-    if (tid == C::NW * 32 - 1) sh.scan_total = before + inc;
+    return v;
+  };
+  if (p.st.n_seqs <= 32) {
+    const long long n = tiles_of(lane), upto = scan(n);
+    T = __shfl_sync(0xffffffffu, upto, 31);
+    if (lane < p.st.n_seqs) prefix[lane] = upto - n;
+    if (lane == 0) prefix[p.st.n_seqs] = T;
+    __syncwarp();
+  } else {
+    if (tid == 0) sh.scan_total = 0;
+    for (int base = 0; base < p.st.n_seqs; base += C::NW * 32) {
+      const int i = base + tid;
+      const long long n = tiles_of(i), upto = scan(n);
+      if (lane == 31) sh.wsum[warp] = upto;
+      __syncthreads();
+      long long before = sh.scan_total;
+      for (int w = 0; w < warp; ++w) before += sh.wsum[w];
+      if (i < p.st.n_seqs) prefix[i] = before + upto - n;
+      __syncthreads();
+      if (tid == C::NW * 32 - 1) sh.scan_total = before + upto;
+      __syncthreads();
+    }
+    T = sh.scan_total;
+    if (tid == 0) prefix[p.st.n_seqs] = T;
     __syncthreads();
   }
-  const long long T = sh.scan_total;
-  if (tid == 0) prefix[p.st.n_seqs] = T;
-  if (tid < 2 * C::NW) sh.meta[tid].id = -1;
-  __syncthreads();
 
-  // rows that see nothing, and the step's errors
-  for (int i = blockIdx.x; i < p.st.n_seqs; i += gridDim.x) {
+  // Tiles of a CTA: a tile for every warp before another CTA takes part, as fewer CTAs have less to join.
+  const bool small = T >> 31 == 0;               // divisions in 32 bits where they can be
+  const long long per = max(small ? static_cast<long long>((static_cast<uint32_t>(T) + gridDim.x - 1) / gridDim.x)
+                                  : (T + gridDim.x - 1) / gridDim.x,
+                            static_cast<long long>(C::NW));
+  const long long c0 = per * blockIdx.x, c1 = max(min(c0 + per, T), c0);
+  const uint32_t share = static_cast<uint32_t>(c1 - c0);
+  const long long w0 = c0 + static_cast<unsigned long long>(share) * warp / C::NW,
+                  w1 = c0 + static_cast<unsigned long long>(share) * (warp + 1) / C::NW;
+  // Rows that see nothing, and the step's errors: the last CTAs, which have the least to do.
+  for (int i = gridDim.x - 1 - blockIdx.x; i < p.st.n_seqs; i += gridDim.x) {
     const SeqSpan s = seq_span(p.st, i);
     if (s.bad && tid == 0) atomicOr(p.st.err, kErrRange);
     if (s.live || s.rows == 0) continue;
@@ -691,12 +714,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     if (p.lse != nullptr)
       for (size_t e = tid; e < n; e += C::NW * 32) p.lse[at + e] = kNegInf;
   }
-
-  // CTAs with work: a tile for every warp before another CTA takes part, as fewer CTAs have less to join
-  const long long n = min(static_cast<long long>(gridDim.x), (T + C::NW - 1) / C::NW);
-  if (blockIdx.x >= n) return;
-  const long long c0 = T * blockIdx.x / n, c1 = T * (blockIdx.x + 1) / n;
-  const long long w0 = c0 + (c1 - c0) * warp / C::NW, w1 = c0 + (c1 - c0) * (warp + 1) / C::NW;
+  if (share == 0) return;
 
   if (w0 < w1) {
     Cursor c, ahead;
@@ -788,7 +806,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     return s & 1 ? reinterpret_cast<const float*>(sh.stage[s >> 1][0])
                  : static_cast<const float*>(p.frag + static_cast<size_t>(blockIdx.x * C::NW + (s >> 1)) * (C::FREG * 32));
   };
-  auto cta_of = [&](long long tile) { return static_cast<int>(((tile + 1) * n - 1) / T); };
+  auto cta_of = [&](long long tile) {
+    return small ? static_cast<int>(static_cast<uint32_t>(tile) / static_cast<uint32_t>(per)) : static_cast<int>(tile / per);
+  };
   const int n_items = __popc(heads);
 #pragma unroll 1
   for (int v = warp; v < n_items * kUnits; v += C::NW) {
@@ -897,8 +917,7 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const size_t smem = sizeof(Shared<D, NT>) + (static_cast<size_t>(p.st.n_seqs) + 1) * 8;
-  cache_attention_kernel<D, NT><<<p.grid, Cfg<D, NT>::NW * 32, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(cache_attention_kernel<D, NT>, dim3(p.grid), Cfg<D, NT>::NW * 32, smem, stream, p);
 }
 }  // namespace
 

@@ -291,6 +291,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
   for (int i = tid; i < 256; i += C::THREADS) sts16(sh.qx + i * 16, 0, 0, 0, 0);
   for (int i = tid; i < C::KST * BT * 2; i += C::THREADS) sts16(sh.kx[0] + i * 16, 0, 0, 0, 0);
   fence_proxy_async_smem();
+  griddep_launch_dependents();
+  griddep_wait();
   // Tiles of every sequence: a thread counts a sequence's, or a warp where a sequence may have many row tiles; then
   // their prefix sums.
   if (static_cast<long long>(p.st.max_new) * p.group > 4 * C::R) {
@@ -874,8 +876,7 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
-  cache_prefill_kernel<D><<<p.grid, PCfg<D>::THREADS, cache_prefill_smem(D, p.st.n_seqs), stream>>>(p);
-  return cudaGetLastError();
+  return launch_chained(cache_prefill_kernel<D>, dim3(p.grid), PCfg<D>::THREADS, cache_prefill_smem(D, p.st.n_seqs), stream, p);
 }
 
 }  // namespace

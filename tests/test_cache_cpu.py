@@ -140,42 +140,41 @@ def test_step_refuses_wrong_tensors():
 
 # ------------------------------------------------ the attention kernel's split ----
 def _split(tiles, grid, warps):
-    """The kernel's runs: [(cta, warp, first tile, last tile + 1)] of a list of `tiles` tiles."""
-    n = min(tiles, grid)
+    """The kernel's tiles of a CTA, and its runs: [(cta, warp, first tile, last tile + 1)] of a list of `tiles`."""
+    per = max(-(-tiles // grid), warps)
     out = []
-    for c in range(n):
-        c0, c1 = tiles * c // n, tiles * (c + 1) // n
+    for c in range(grid):
+        c0 = per * c
+        c1 = max(min(c0 + per, tiles), c0)
         for w in range(warps):
             a, b = c0 + (c1 - c0) * w // warps, c0 + (c1 - c0) * (w + 1) // warps
             if a < b:
                 out.append((c, w, a, b))
-    return out
+    return per, out
 
 
 @pytest.mark.parametrize("seed", range(40))
 def test_work_split_covers_the_list_once_and_counts_arrivals(seed):
     gen = np.random.default_rng(seed)
-    grid, warps = 148, 12
+    grid, warps = 148, int(gen.choice([8, 12]))
     items = gen.integers(1, int(gen.choice([2, 5, 60, 3000])), size=int(gen.integers(1, 200)))
     begin = np.concatenate([[0], np.cumsum(items)])
     T = int(begin[-1])
-    n = min(T, grid)
-    runs = _split(T, grid, warps)
+    per, runs = _split(T, grid, warps)
     assert [r[2] for r in runs[1:]] == [r[3] for r in runs[:-1]] and runs[0][2] == 0 and runs[-1][3] == T
-    starts = [T * i // n for i in range(n + 1)]
     counts = {}
     for i, size in enumerate(items):
         a, b = int(begin[i]), int(begin[i + 1])
         ctas = sorted({c for c, _, x, y in runs if x < b and y > a})
-        f0, f1 = ((a + 1) * n - 1) // T, ((b - 1 + 1) * n - 1) // T     # the kernel's cta_of
-        assert ctas == list(range(f0, f1 + 1))
+        f0, f1 = a // per, (b - 1) // per                               # the kernel's cta_of
+        assert ctas == list(range(f0, f1 + 1)) and f1 < grid
         if f1 > f0:
             # the counter of CTA f0 belongs to this item alone, and every CTA of it has a part of its own
             assert f0 not in counts
             counts[f0] = i
-            assert starts[f0] <= a
+            assert per * f0 <= a
             for c in range(f0 + 1, f1 + 1):
-                assert starts[c] > a          # parts 2 c of the later ones, 2 f0 + 1 of the first
+                assert per * c > a            # parts 2 c of the later ones, 2 f0 + 1 of the first
     # a warp holds at most two partial results: of its run's first and last item
     for c, w, x, y in runs:
         cut = [i for i in range(len(items)) if begin[i] < y and begin[i + 1] > x and not (x <= begin[i] and begin[i + 1] <= y)]
