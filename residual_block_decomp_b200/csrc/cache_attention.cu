@@ -550,22 +550,18 @@ struct State {
     }
   }
 
-  // [register][lane] floats
+  // [four registers][lane] float4: the accumulators, then (m, m, l, l) of the row blocks' columns
   __device__ void store(float* f, int lane) const {
-    int r = 0;
+    float4* to = reinterpret_cast<float4*>(f) + lane;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < C::J; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) f[(r++) * 32 + lane] = o[nt][j][e / 4][e % 4];
+        for (int e = 0; e < 4; ++e)
+          to[((nt * C::J + j) * 4 + e) * 32] = make_float4(o[nt][j][e][0], o[nt][j][e][1], o[nt][j][e][2], o[nt][j][e][3]);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      f[(r++) * 32 + lane] = m[nt][0];
-      f[(r++) * 32 + lane] = m[nt][1];
-      f[(r++) * 32 + lane] = l[nt][0];
-      f[(r++) * 32 + lane] = l[nt][1];
-    }
+    for (int nt = 0; nt < NT; ++nt) to[(C::OREG / 4 + nt) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
   }
 };
 
@@ -593,51 +589,80 @@ __device__ __forceinline__ void write_row(const CacheAttnParams& p, const Item& 
 }
 
 // Joins partial results first, first + step, ... < n of an item (addresses from `at(i)`), in that order, for
-// one block of registers: row block nt, word j, column k (8 numbers of one row per lane).  Four are
-// loaded at a time.
+// one block of registers, row block nt and word j: 8 numbers each of two rows (columns) a lane.  Two are loaded at a
+// time.
+struct Joined {
+  float4 x[4], ml;   // x[e]: dim e of both columns, dim 4 + e of both; m, m, l, l
+};
 template <int D, int NT, typename At>
-__device__ __forceinline__ void join(int first, int step, int n, const At& at, int nt, int j, int k, int lane, float (&x)[8],
-                                     float& m, float& l) {
+__device__ __forceinline__ Joined join(int first, int step, int n, const At& at, int nt, int j, int lane) {
   using C = Cfg<D, NT>;
-  const int mr = (C::OREG + nt * 4 + k) * 32 + lane, r0 = ((nt * C::J + j) * 16 + k) * 32 + lane;
-  m = kNothing;
-  l = 0.0f;
+  constexpr int B = 2;
+  const int r0 = (nt * C::J + j) * 128 + lane, mr = (C::OREG / 4 + nt) * 32 + lane;
+  Joined r;
+  r.ml = make_float4(kNothing, kNothing, 0.0f, 0.0f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = 0.0f;
+  for (int e = 0; e < 4; ++e) r.x[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-  for (int i = first; i < n; i += 4 * step) {
-    float fm[4], fl[4], fx[4][8];
+  for (int i = first; i < n; i += B * step) {
+    float4 ml[B], x[B][4];
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      fm[b] = kNothing;
-      fl[b] = 0.0f;
+    for (int b = 0; b < B; ++b) {
+      ml[b] = make_float4(kNothing, kNothing, 0.0f, 0.0f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) fx[b][e] = 0.0f;
+      for (int e = 0; e < 4; ++e) x[b][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (i + b * step < n) {
-        const float* f = at(i + b * step);
-        fm[b] = f[mr];
-        fl[b] = f[mr + 64];
+        const float4* f = reinterpret_cast<const float4*>(at(i + b * step));
+        ml[b] = f[mr];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          fx[b][e] = f[r0 + e * 128];            // dim 8 w + e
-          fx[b][4 + e] = f[r0 + e * 128 + 64];   // dim 8 w + 4 + e
-        }
+        for (int e = 0; e < 4; ++e) x[b][e] = f[r0 + e * 32];
       }
     }
-    const float top = fmaxf(fmaxf(m, fmaxf(fm[0], fm[1])), fmaxf(fm[2], fm[3]));
-    const float keep = ex2(m - top);
-    m = top;
-    l *= keep;
+    const float m0 = fmaxf(r.ml.x, fmaxf(ml[0].x, ml[1].x)), m1 = fmaxf(r.ml.y, fmaxf(ml[0].y, ml[1].y));
+    const float k0 = ex2(r.ml.x - m0), k1 = ex2(r.ml.y - m1);
+    r.ml = make_float4(m0, m1, r.ml.z * k0, r.ml.w * k1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= keep;
+    for (int e = 0; e < 4; ++e) r.x[e] = make_float4(r.x[e].x * k0, r.x[e].y * k1, r.x[e].z * k0, r.x[e].w * k1);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float w = ex2(fm[b] - top);
-      l = fmaf(w, fl[b], l);
+    for (int b = 0; b < B; ++b) {
+      const float w0 = ex2(ml[b].x - m0), w1 = ex2(ml[b].y - m1);
+      r.ml.z = fmaf(w0, ml[b].z, r.ml.z);
+      r.ml.w = fmaf(w1, ml[b].w, r.ml.w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(w, fx[b][e], x[e]);
+      for (int e = 0; e < 4; ++e) {
+        r.x[e].x = fmaf(w0, x[b][e].x, r.x[e].x);
+        r.x[e].y = fmaf(w1, x[b][e].y, r.x[e].y);
+        r.x[e].z = fmaf(w0, x[b][e].z, r.x[e].z);
+        r.x[e].w = fmaf(w1, x[b][e].w, r.x[e].w);
+      }
     }
   }
+  return r;
+}
+// Both rows of a joined block to the output.
+template <int D, int NT>
+__device__ __forceinline__ void write_joined(const CacheAttnParams& p, const FragMeta& fm, int nt, int j, const Joined& r, int lane) {
+  float y[8];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e] = r.x[e].x;
+    y[4 + e] = r.x[e].z;
+  }
+  write_row<D, NT>(p, fm, nt, 0, (lane >> 2) + 8 * j, y, r.ml.x, r.ml.z, lane);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    y[e] = r.x[e].y;
+    y[4 + e] = r.x[e].w;
+  }
+  write_row<D, NT>(p, fm, nt, 1, (lane >> 2) + 8 * j, y, r.ml.y, r.ml.w, lane);
+}
+template <int D, int NT>
+__device__ __forceinline__ void store_joined(float* f, int nt, int j, const Joined& r, int lane) {
+  using C = Cfg<D, NT>;
+  float4* to = reinterpret_cast<float4*>(f) + lane;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) to[((nt * C::J + j) * 4 + e) * 32] = r.x[e];
+  if (j == 0) to[(C::OREG / 4 + nt) * 32] = r.ml;
 }
 
 template <int D, int NT>
@@ -795,7 +820,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
 
   // Join what warps share; of what CTAs share write this CTA's part.  Slots are in the order of the list, so an
   // item's are neighbours: every warp finds the items' first slots by vote.
-  constexpr int kUnits = NT * C::J * 2;
+  constexpr int kUnits = NT * C::J;              // blocks of registers: 8 numbers of two rows a lane
   static_assert(2 * C::NW <= 32, "a lane a slot");
   const long long my_id = lane < 2 * C::NW ? sh.meta[lane].id : -1;
   const uint32_t present = __ballot_sync(0xffffffffu, my_id >= 0);
@@ -819,30 +844,18 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     uint32_t slots = present >> head << head;
     if (hm != 0) slots &= (hm & -hm) - 1;
     const FragMeta& fm = sh.meta[head];
-    const int u = v % kUnits, k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
-    float x[8], m, l;
-    join<D, NT>(0, 1, __popc(slots),
-                [&](int) {                     // asked for in order
-                  const int s = __ffs(slots) - 1;
-                  slots &= slots - 1;
-                  return slot_at(s);
-                },
-                nt, j, k, lane, x, m, l);
-    if (fm.id >= c0 && fm.id + fm.tiles <= c1) {
-      write_row<D, NT>(p, fm, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
-    } else {
-      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (fm.id >= c0 ? 1 : 0)) * (C::FREG * 32);
-      const int r0 = ((nt * C::J + j) * 16 + k) * 32 + lane, mr = (C::OREG + nt * 4 + k) * 32 + lane;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        part[r0 + e * 128] = x[e];
-        part[r0 + e * 128 + 64] = x[4 + e];
-      }
-      if (j == 0) {
-        part[mr] = m;
-        part[mr + 64] = l;
-      }
-    }
+    const int u = v % kUnits, j = u % C::J, nt = u / C::J;
+    const Joined r = join<D, NT>(0, 1, __popc(slots),
+                                 [&](int) {    // asked for in order
+                                   const int s = __ffs(slots) - 1;
+                                   slots &= slots - 1;
+                                   return slot_at(s);
+                                 },
+                                 nt, j, lane);
+    if (fm.id >= c0 && fm.id + fm.tiles <= c1)
+      write_joined<D, NT>(p, fm, nt, j, r, lane);
+    else
+      store_joined<D, NT>(p.part + static_cast<size_t>(blockIdx.x * 2 + (fm.id >= c0 ? 1 : 0)) * (C::FREG * 32), nt, j, r, lane);
   }
   if (tid < 2) sh.last[tid] = -1;
   __syncthreads();
@@ -864,41 +877,45 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
   }
   __syncthreads();
   constexpr int kGroups = C::NW / kUnits;      // warps of a block of registers share the parts
-  float* scratch = reinterpret_cast<float*>(sh.stage);
+  float4* scratch = reinterpret_cast<float4*>(sh.stage);
+  static_assert(2 * C::NW * 2560 <= sizeof(sh.stage), "the groups' results");
 #pragma unroll 1
   for (int it = 0; it < 2; ++it) {
     const int slot = sh.last[it];
     if (slot < 0) continue;
     const FragMeta& fm = sh.meta[slot];
     const int f0 = cta_of(fm.id), parts = cta_of(fm.id + fm.tiles - 1) - f0 + 1;
-    const int u = warp % kUnits, grp = warp / kUnits, k = u & 1, j = (u >> 1) % C::J, nt = (u >> 1) / C::J;
+    const int u = warp % kUnits, grp = warp / kUnits, j = u % C::J, nt = u / C::J;
     const float* base = p.part + static_cast<size_t>(f0) * 2 * (C::FREG * 32);
-    float x[8], m, l;
+    Joined r;
     if (grp < kGroups)
-      join<D, NT>(grp, kGroups, parts, [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? 1 : 0)) * (C::FREG * 32); },
-                  nt, j, k, lane, x, m, l);
+      r = join<D, NT>(grp, kGroups, parts, [&](int i) { return base + static_cast<size_t>(2 * i + (i == 0 ? 1 : 0)) * (C::FREG * 32); },
+                      nt, j, lane);
     if (kGroups > 1) {
-      float* mine = scratch + (it * C::NW + warp) * 320 + lane;
+      float4* mine = scratch + (it * C::NW + warp) * 160 + lane;
       if (grp > 0 && grp < kGroups) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mine[e * 32] = x[e];
-        mine[256] = m;
-        mine[288] = l;
+        for (int e = 0; e < 4; ++e) mine[e * 32] = r.x[e];
+        mine[128] = r.ml;
       }
       __syncthreads();
       if (grp == 0) {
 #pragma unroll 1
         for (int g = 1; g < kGroups; ++g) {
-          const float* f = scratch + (it * C::NW + g * kUnits + u) * 320 + lane;
-          const float top = fmaxf(m, f[256]), keep = ex2(m - top), w = ex2(f[256] - top);
-          m = top;
-          l = l * keep + w * f[288];
+          const float4* f = scratch + (it * C::NW + g * kUnits + u) * 160 + lane;
+          const float4 ml = f[128];
+          const float m0 = fmaxf(r.ml.x, ml.x), m1 = fmaxf(r.ml.y, ml.y);
+          const float k0 = ex2(r.ml.x - m0), k1 = ex2(r.ml.y - m1), w0 = ex2(ml.x - m0), w1 = ex2(ml.y - m1);
+          r.ml = make_float4(m0, m1, r.ml.z * k0 + w0 * ml.z, r.ml.w * k1 + w1 * ml.w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = x[e] * keep + w * f[e * 32];
+          for (int e = 0; e < 4; ++e) {
+            const float4 x = f[e * 32];
+            r.x[e] = make_float4(r.x[e].x * k0 + w0 * x.x, r.x[e].y * k1 + w1 * x.y, r.x[e].z * k0 + w0 * x.z, r.x[e].w * k1 + w1 * x.w);
+          }
         }
       }
     }
-    if (grp == 0) write_row<D, NT>(p, fm, nt, k, (lane >> 2) + 8 * j, x, m, l, lane);
+    if (grp == 0) write_joined<D, NT>(p, fm, nt, j, r, lane);
   }
 }
 
