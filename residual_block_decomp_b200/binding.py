@@ -350,6 +350,7 @@ def bs_cache_destroy(handle: int) -> None:
     _cache_shapes.pop(handle, None)
 
 
+_NO_CACHE = (None, None, None)
 _cache_shapes: dict[int, tuple] = {}   # (heads, dim, device) of live handles, for the tensors' checks
 
 
@@ -386,13 +387,14 @@ class CacheStep:
 def _rows(t, name: str, handle: int, step: CacheStep, query: bool = False) -> tuple:
     """(pointer, token stride, head stride) of a tensor [n_tokens, heads, dim] with contiguous numbers
     on the cache's GPU; a query's heads are a multiple of the cache's (checked by the library)."""
-    heads, dim, device = _cache_shapes.get(handle, (None, None, None))
-    if t.dim() != 3 or t.shape[0] != step.n_tokens or t.shape[2] != dim or not (query or t.shape[1] == heads):
-        raise ValueError(f"{name}: need [{step.n_tokens}, {'q_heads' if query else heads}, {dim}], got {list(t.shape)}")
+    heads, dim, device = _cache_shapes.get(handle, _NO_CACHE)
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != step.n_tokens or shape[2] != dim or (shape[1] != heads and not query):
+        raise ValueError(f"{name}: need [{step.n_tokens}, {'q_heads' if query else heads}, {dim}], got {list(shape)}")
     tok, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name}: the numbers of a head must be contiguous")
-    if t.device != device or step.device != device:
+    if t.device != device or step.device is not device and step.device != device:
         raise ValueError(f"{name}: tensors and step must be on the cache's device {device}")
     return t.data_ptr(), tok, head
 
@@ -402,21 +404,23 @@ def bs_cache_append(handle: int, step: CacheStep, k, v, stream=None) -> None:
     pages of the step's positions."""
     if k.dtype != v.dtype:
         raise ValueError("k and v must have one dtype")
-    st = lib.bs_cache_append(handle, step.ref, *_rows(k, "k", handle, step), *_rows(v, "v", handle, step),
-                             _dtype_code(k), _stream(stream))
+    kp, kt, kh = _rows(k, "k", handle, step)
+    vp, vt, vh = _rows(v, "v", handle, step)
+    st = lib.bs_cache_append(handle, step.ref, kp, kt, kh, vp, vt, vh, _dtype_code(k), _stream(stream))
     _check(st, "bs_cache_append")
 
 
 def bs_cache_read(handle: int, step: CacheStep, k_out, v_out, stream=None) -> None:
     """Writes the numbers stored at the step's positions to k_out and v_out (contiguous
     [n_tokens, heads, dim]; either may be None)."""
-    outs = [t for t in (k_out, v_out) if t is not None]
-    for t in outs:
-        _rows(t, "k_out, v_out", handle, step)
-        if not t.is_contiguous() or t.dtype != outs[0].dtype:
-            raise ValueError("k_out and v_out must be contiguous and of one dtype")
-    st = lib.bs_cache_read(handle, step.ref, _ptr(k_out), _ptr(v_out), _dtype_code(outs[0]) if outs else 0,
-                           _stream(stream))
+    ptr = [None, None]
+    first = k_out if k_out is not None else v_out
+    for i, t in enumerate((k_out, v_out)):
+        if t is not None:
+            ptr[i] = _rows(t, "k_out, v_out", handle, step)[0]
+            if not t.is_contiguous() or t.dtype != first.dtype:
+                raise ValueError("k_out and v_out must be contiguous and of one dtype")
+    st = lib.bs_cache_read(handle, step.ref, ptr[0], ptr[1], 0 if first is None else _dtype_code(first), _stream(stream))
     _check(st, "bs_cache_read")
 
 
