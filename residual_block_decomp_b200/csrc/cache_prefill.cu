@@ -18,7 +18,8 @@
 // as the rounding of P does, and the lse, which is fp32, by more than fp32 allows.  Values are rounded to fp16 by
 // one fma.
 //
-// Roles: 8 warps own the rows, two threads a row with half a tile's tokens each (softmax, output); one warp walks the list
+// Roles: 8 warps own 16 rows each (softmax, output): they take S and O in the shape in which four neighbouring lanes hold a
+// row, so that a row's maximum is two shuffles and no warp waits for another; one warp walks the list
 // and has the packed tiles copied ahead (one bulk copy a chunk); 8 warps expand them, the keys of tile t + 1 before the
 // values of tile t, whose stage waits for tile t - 1's products; one thread issues all products, S of tile t before O of
 // tile t - 1, so that the tensor pipe works on the next tile while the rows are at this one's softmax.
@@ -78,7 +79,8 @@ struct alignas(1024) PShared {
   uint8_t qx[128 * 32];                     // the 16 columns of sums and of b: core matrices of 8 rows x 16 bytes
   uint8_t kx[C::KST][C::BT * 32];
   uint8_t staging[2][2][C::HALF_BYTES];     // packed keys, packed values: of the tile in use and of the next
-  float half[2][2][128];                    // what a row's two threads tell each other
+  uint32_t top[2][128];                     // loading Q: the largest entries of a row's halves
+  float factor[128];                        // a row's score factor
   uint64_t kfull[C::KST], kempty[C::KST], vfull[C::VST], vempty[C::VST];
   uint64_t qfull, sfull[2], pfull[2], pvdone[2], drained;
   uint64_t cfull[2][2], cempty[2][2];       // staging: [keys, values][slot]
@@ -228,27 +230,56 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 16 lanes x 64 columns: register 4 n + e of lane 4 r + c holds row r + 8 (e / 2), column 8 n + 2 c + e % 2.
+__device__ __forceinline__ void tmem_ld_rows(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_rows(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 16 lanes x 32 columns: register 2 n + e of lane 4 r + c holds row r + 8 e, column 4 n + c: pairs of the above, packed.
+__device__ __forceinline__ void tmem_st_pairs(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void sts16(uint8_t* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
 }
 // Unit (16 bytes) w of row r in a block of 128-byte rows.
 __device__ __forceinline__ int swz(int r, int w) { return r * 128 + ((w ^ (r & 7)) << 4); }
 
-// Writes 8 numbers of a row (words w) to out, in the order of O's columns.
-__device__ __forceinline__ uint4 out_word(const float (&x)[8], float inv, int bf16) {
-  // columns hold dims 0, 4, 1, 5, 2, 6, 3, 7
-  const float y[8] = {x[0] * inv, x[2] * inv, x[4] * inv, x[6] * inv, x[1] * inv, x[3] * inv, x[5] * inv, x[7] * inv};
-  uint32_t r[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (bf16) {
-      const __nv_bfloat162 h = __floats2bfloat162_rn(y[2 * e], y[2 * e + 1]);
-      r[e] = *reinterpret_cast<const uint32_t*>(&h);
-    } else {
-      r[e] = h2u(__floats2half2_rn(y[2 * e], y[2 * e + 1]));
-    }
+// A word of a row from the four lanes that hold it: lane c has columns 2 c, 2 c + 1, which are dims c and c + 4; it
+// writes dims 2 c and 2 c + 1.
+__device__ __forceinline__ void write_word(uint16_t* row, int w, float a, float b, int bf16, bool there, int lane) {
+  uint32_t mine;
+  if (bf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    mine = *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    mine = h2u(__floats2half2_rn(a, b));
   }
-  return make_uint4(r[0], r[1], r[2], r[3]);
+  const int from = (lane & ~3) + 2 * (lane & 1);
+  const uint32_t u = __shfl_sync(0xffffffffu, mine, from), v = __shfl_sync(0xffffffffu, mine, from + 1);
+  if (there) reinterpret_cast<uint32_t*>(row + 8 * w)[lane & 3] = __byte_perm(u, v, lane & 2 ? 0x7632 : 0x5410);
 }
 
 template <int D>
@@ -360,98 +391,87 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 
   if (warp < kRowWarps) {
     // ------------------------------------------------------------ rows: softmax and output
-    // Thread (r, hf): row r, tokens hf BT / 2 .. of a tile, output columns hf D / 2 ..
-    const int r = (warp & 3) * 32 + lane, hf = warp >> 2;
-    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    const uint32_t o_at = lanes + C::O_COL + hf * (D / 2);
+    // Warp (quadrant, hf): rows 32 quadrant + 16 hf .. of the item, two a lane; for Q the quadrant's 32 rows, a lane a row,
+    // and half hf of its numbers.
+    const int quadrant = warp & 3, hf = warp >> 2;
+    const uint32_t quad_at = tmem + (static_cast<uint32_t>(quadrant * 32) << 16);
+    const uint32_t lanes = quad_at + (static_cast<uint32_t>(hf * 16) << 16);
     uint32_t i = 0;                                             // tiles so far: phases of all barriers
     bool ok = true;
-    // The two warps of the same rows meet: what either wrote to shared memory before is there for the other, and either
-    // knows whether one of them said so, or gave up (then both do).
+    // The two warps of a quadrant meet: what either wrote to shared memory before is there for the other, and both know
+    // whether one gave up.
     uint32_t met = 0;
-    auto meet = [&](bool said) {
-      said = __any_sync(0xffffffffu, said);
+    auto meet = [&]() {
+      __syncwarp();
       if (lane == 0) {
-        *reinterpret_cast<volatile int*>(&sh.say[met & 1][warp]) = (said ? 1 : 0) | (ok ? 0 : 2);
-        mbar_arrive(&sh.pair[warp & 3]);
+        *reinterpret_cast<volatile int*>(&sh.say[met & 1][warp]) = ok ? 0 : 1;
+        mbar_arrive(&sh.pair[quadrant]);
       }
       __syncwarp();
-      ok = wait(&sh.pair[warp & 3], met) && ok;
-      const int other = *reinterpret_cast<volatile int*>(&sh.say[met & 1][warp ^ 4]);
-      if (other & 2) ok = false;
+      ok = wait(&sh.pair[quadrant], met) && ok;
+      if (*reinterpret_cast<volatile int*>(&sh.say[met & 1][warp ^ 4]) != 0) ok = false;
       ++met;
-      return said || (other & 1) != 0;
     };
     Segment sg{};
     if (works) sg = list.at(c0, c1, lane);
     for (long long tile = c0; tile < c1 && ok; list.next(sg, c1, lane)) {
       tile = sg.id + sg.t1;
-      const int row = sg.rt * C::R + r, total = sg.rows * p.group;
-      const bool there = row < total;
-      const int tok = row / p.group, hq = sg.h * p.group + row % p.group;
-      const int pos = there ? sg.start + tok : -1;
-      const int low = there ? pos - p.window : -1;              // positions at or below it are hidden
+      const int total = sg.rows * p.group;
       const int lowest = sg.start + sg.rt * C::R / p.group, highest = sg.end - 1;
-      float f;
       {
-        // the row as fp16, its largest entry in [1, 2), into tensor memory; sums over groups, halved, into qx.  A
-        // thread takes half of the row, all loads at once.
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (sg.row0 + tok) * p.q_tok +
-                                                          static_cast<long long>(hq) * p.q_head) + hf * (D / 16);
-        uint4 raw[D / 16];
-#pragma unroll
-        for (int w = 0; w < D / 16; ++w) raw[w] = there ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
-        auto two = [&](uint32_t x) {
-          return p.bf16 ? make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)) : __half22float2(u2h(x));
-        };
+        // a row as fp16, its largest entry in [1, 2), into tensor memory; sums over groups, halved, into qx.  (Loops are
+        // kept as loops: this runs once an item, and instructions that run once are fetched at memory's pace.)
+        const int r = quadrant * 32 + lane, row = sg.rt * C::R + r;
+        const bool there = row < total;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.q) + (sg.row0 + row / p.group) * p.q_tok +
+                                                          static_cast<long long>(sg.h * p.group + row % p.group) * p.q_head) + hf * (D / 16);
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
         for (int w = 0; w < D / 16; ++w) {
-          const uint32_t x[4] = {raw[w].x, raw[w].y, raw[w].z, raw[w].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 v = two(x[e]);
-            top = max(top, max(__float_as_uint(v.x) & 0x7f800000u, __float_as_uint(v.y) & 0x7f800000u));
-          }
+          const uint4 a = there ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+          top = __vmaxu2(__vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu)), top);
         }
-        sh.half[0][hf][r] = __uint_as_float(top);
-        __syncwarp();
-        meet(false);
-        top = max(top, __float_as_uint(sh.half[0][hf ^ 1][r]));
-        meet(false);                                            // `half` is free for the tiles
-        const int ex = static_cast<int>(top >> 23);
+        top = max(top & 0xffffu, top >> 16);
+        sh.top[hf][r] = top;
+        meet();
+        if (!ok) break;
+        top = max(top, sh.top[hf ^ 1][r]);
+        const uint32_t bits = p.bf16 ? top << 16 : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(top))));
+        const int ex = static_cast<int>(bits >> 23);
         const int up = min(max(254 - ex, 1), 254);
         float scale = __uint_as_float(static_cast<uint32_t>(up) << 23);
-        f = fmaxf(ldexpf(fabsf(p.scale_log2), 128 - up), 0x1p-120f);   // 2 for the halved keys
-        if (ex == 255) {                                        // a row with inf or NaN is NaN
-          f = __int_as_float(0x7fffffff);
-          scale = 0.0f;
-        }
+        float f = fmaxf(ldexpf(fabsf(p.scale_log2), 128 - up), 0x1p-120f);   // 2 for the halved keys
+        if (ex == 255) f = __int_as_float(0x7fffffff);          // a row with inf or NaN is NaN
         if (p.scale_log2 < 0.0f) scale = -scale;
         if (p.scale_log2 == 0.0f) scale = 0.0f;
-#pragma unroll
+        if (hf == 0) sh.factor[r] = f;
+#pragma unroll 1
         for (int g = 0; g < C::GR / 2; ++g) {
           const int gr = hf * (C::GR / 2) + g;
+          uint4 raw[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) raw[k] = there && ex != 255 ? __ldg(src + 4 * g + k) : make_uint4(0, 0, 0, 0);
           float sum = 0.0f;
           uint32_t cols[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint4 a = raw[4 * g + k];
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w};
-            float y[8];
+            const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            uint32_t h[4];                                      // dims 2 e, 2 e + 1
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 v = two(x[e]);
-              const __half2 h = ex == 255 ? __floats2half2_rn(0.0f, 0.0f) : __floats2half2_rn(v.x * scale, v.y * scale);
-              const float2 b = __half22float2(h);
+              const float2 v = p.bf16 ? make_float2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)) : __half22float2(u2h(x[e]));
+              const __half2 y = __floats2half2_rn(v.x * scale, v.y * scale);
+              const float2 b = __half22float2(y);
               sum += b.x + b.y;
-              y[2 * e] = b.x;
-              y[2 * e + 1] = b.y;
+              h[e] = h2u(y);
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) cols[4 * k + e] = h2u(__floats2half2_rn(y[e], y[e + 4]));
+            cols[4 * k] = __byte_perm(h[0], h[2], 0x5410);
+            cols[4 * k + 1] = __byte_perm(h[0], h[2], 0x7632);
+            cols[4 * k + 2] = __byte_perm(h[1], h[3], 0x5410);
+            cols[4 * k + 3] = __byte_perm(h[1], h[3], 0x7632);
           }
-          tmem_st16(lanes + C::Q_COL + gr * 16, cols);
+          __syncwarp();
+          tmem_st16(quad_at + C::Q_COL + gr * 16, cols);
           sum *= 0.5f;
           const __half hi = __float2half_rn(sum), lo = __float2half_rn(sum - __half2float(hi));
           auto put = [&](int col, __half x) {
@@ -465,130 +485,156 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.qfull);
+        meet();                                                 // the rows' factors
+        if (!ok) break;
       }
-      float m = kNothing, l = 0.0f;
+      // the lane's two rows
+      float f[2], m[2], l[2];
+      int pos[2], low[2];
+      size_t at[2];
+      bool there[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = quadrant * 32 + hf * 16 + (lane >> 2) + 8 * k, row = sg.rt * C::R + r;
+        there[k] = row < total;
+        const int tok = row / p.group;
+        pos[k] = there[k] ? sg.start + tok : -1;
+        low[k] = there[k] ? pos[k] - p.window : -1;             // positions at or below it are hidden
+        at[k] = static_cast<size_t>(sg.row0 + tok) * p.q_heads + sg.h * p.group + row % p.group;
+        f[k] = sh.factor[r];
+        m[k] = kNothing;
+        l[k] = 0.0f;
+      }
       for (int t = sg.t0; t < sg.t1; ++t, ++i) {
         const int buf = i & 1;
-        const uint32_t s_at = lanes + buf * BT + hf * (BT / 2);
-        const int pos0 = sg.first + t * BT + hf * (BT / 2);     // of the thread's first token
-        ok = wait(&sh.sfull[buf], i >> 1) && ok;
+        const uint32_t s_at = lanes + buf * BT;
+        const int pos0 = sg.first + t * BT;
+        ok = wait(&sh.sfull[buf], i >> 1);
+        if (!ok) break;
         tc_fence_after();
-        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 7]) >> (hf * C::CHUNKS / 2) & ((1 << C::CHUNKS / 2) - 1);
-        const bool masked = pos0 + BT / 2 - 1 > lowest || pos0 <= highest - p.window || good != (1 << C::CHUNKS / 2) - 1;
-        // Hidden scores become -inf: tokens
-        // behind the row's own, those the window leaves out, chunks outside the pool.
-        const int above = pos - pos0, under = low - pos0;
-        uint32_t x[BT / 64][32];
-#pragma unroll
-        for (int c = 0; c < BT / 64; ++c) tmem_ld32(s_at + c * 32, x[c]);
-        tc_wait_ld();
-        if (masked) {
-#pragma unroll
-          for (int c = 0; c < BT / 64; ++c)
+        const int good = *reinterpret_cast<volatile int*>(&sh.good[i & 7]);
+        const bool masked = pos0 + BT - 1 > lowest || pos0 <= highest - p.window || good != (1 << C::CHUNKS) - 1;
+        // 64 tokens at a time, twice: for the maximum, and for the weights.  Hidden scores become -inf: tokens behind the
+        // row's own, those the window leaves out, chunks outside the pool.
+        uint32_t x[32];
+        auto load = [&](int c) {
+          tmem_ld_rows(s_at + c, x);
+          tc_wait_ld();
+          if (masked) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
-              const int k = c * 32 + j;
-              if (k > above || k <= under || !((good >> (k / 16)) & 1)) x[c][j] = 0xff800000u;
+              const int col = c + (j >> 2) * 8 + 2 * (lane & 3) + (j & 1), k = (j >> 1) & 1;
+              if (pos0 + col > pos[k] || pos0 + col <= low[k] || !((good >> (col >> 4)) & 1)) x[j] = 0xff800000u;
             }
+          }
+        };
+        float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll 1
+        for (int c = 0; c < BT; c += 64) {
+          load(c);
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            top[0] = fmaxf(top[0], fmaxf(__uint_as_float(x[j]), __uint_as_float(x[j + 1])));
+            top[1] = fmaxf(top[1], fmaxf(__uint_as_float(x[j + 2]), __uint_as_float(x[j + 3])));
+          }
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < BT / 64; ++c)
+        for (int k = 0; k < 2; ++k) {
+          top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+          top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2)) * f[k];
+        }
+        if (__any_sync(0xffffffffu, top[0] > m[0] + kLag || top[1] > m[1] + kLag)) {
+          float keep[2];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(x[c][j]));
-        float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f;
-        // The two warps of the same rows go on together when none of their scores passes the reference; else they
-        // tell each other the rows' maxima.
-        const bool passed = meet(top > m + kLag);
-        if (!ok) break;
-        if (passed) {
-          sh.half[buf][hf][r] = top;
-          __syncwarp();
-          meet(false);
-          if (!ok) break;
-          top = fmaxf(top, sh.half[buf][hf ^ 1][r]);
-          const float mn = top > m + kLag ? top : m;
-          const float keep = ex2(m - mn);
-          l *= keep;
-          m = mn;
+          for (int k = 0; k < 2; ++k) {
+            const float mn = top[k] > m[k] + kLag ? top[k] : m[k];
+            keep[k] = ex2(m[k] - mn);
+            l[k] *= keep[k];
+            m[k] = mn;
+          }
           if (t > sg.t0) {                                      // O of this item exists once the tile before is added
-            ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);   // (a failure is seen at the next barrier)
+            ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);
+            if (!ok) break;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 2; c += 16) {
-              uint32_t o[16];
-              tmem_ld16(o_at + c, o);
+            for (int c = 0; c < D; c += 64) {
+              tmem_ld_rows(lanes + C::O_COL + c, x);
               tc_wait_ld();
 #pragma unroll
-              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-              tmem_st16(o_at + c, o);
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * keep[(j >> 1) & 1]);
+              tmem_st_rows(lanes + C::O_COL + c, x);
             }
           }
         }
-        float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int c = 0; c < BT / 64; ++c) {
+#pragma unroll 1
+        for (int c = 0; c < BT; c += 64) {
+          load(c);
           uint32_t pr[16];
 #pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            const float a = ex2(fmaf(__uint_as_float(x[c][j]), f, -m)), b = ex2(fmaf(__uint_as_float(x[c][j + 1]), f, -m));
-            l4[j & 2] += a;
-            l4[(j & 2) + 1] += b;
+          for (int j = 0; j < 32; j += 4) {
+            const float a = ex2(fmaf(__uint_as_float(x[j]), f[0], -m[0])), b = ex2(fmaf(__uint_as_float(x[j + 1]), f[0], -m[0]));
+            const float d = ex2(fmaf(__uint_as_float(x[j + 2]), f[1], -m[1])), e = ex2(fmaf(__uint_as_float(x[j + 3]), f[1], -m[1]));
+            l[0] += a + b;
+            l[1] += d + e;
             pr[j / 2] = h2u(__floats2half2_rn(a, b));
+            pr[j / 2 + 1] = h2u(__floats2half2_rn(d, e));
           }
-          tmem_st16(s_at + c * 16, pr);                         // over scores of this thread
+          tmem_st_pairs(s_at + c / 2, pr);                      // over scores of these rows that have been read
         }
-        l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
         tc_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.pfull[buf]);
       }
+      if (!ok) break;
       // The segment's O: all of the item, or this CTA's part of it.  (Two barriers for the tiles' ends, as that of tile
       // i - 1 may or may not have been waited for: the one two tiles before it is over for sure when S of
       // tile i is there, so a parity never stands for an older phase.)
-      ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1) && ok;
-      sh.half[i & 1][hf][r] = l;                                // read at this parity's barrier below, written next two tiles on
-      __syncwarp();
-      meet(false);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
+      }
+      ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);
       if (!ok) break;
-      l += sh.half[i & 1][hf ^ 1][r];
       tc_fence_after();
       const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
-      const size_t at = static_cast<size_t>(sg.row0 + tok) * p.q_heads + hq;
-      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R) + r;
-      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
+      float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R);
+      uint16_t* out = static_cast<uint16_t*>(p.out);
+      float inv[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) inv[k] = l[k] > 0.0f ? 1.0f / l[k] : (l[k] == 0.0f ? 0.0f : l[k]);
 #pragma unroll 1
-      for (int c = 0; c < D / 2; c += 32) {
-        const int col = hf * (D / 2) + c;
+      for (int c = 0; c < D; c += 64) {
         uint32_t o[32];
-        tmem_ld32(o_at + c, o);
+        tmem_ld_rows(lanes + C::O_COL + c, o);
         tc_wait_ld();
         if (whole) {
-          if (there) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              float y[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(o[8 * w + e]);
-              reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[col / 8 + w] = out_word(y, inv, p.bf16);
-            }
+          for (int j = 0; j < 32; j += 2) {
+            const int k = (j >> 1) & 1;
+            write_word(out + at[k] * D, (c >> 3) + (j >> 2), __uint_as_float(o[j]) * inv[k], __uint_as_float(o[j + 1]) * inv[k], p.bf16,
+                       there[k], lane);
           }
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) part[(col + j) * C::R] = __uint_as_float(o[j]);
+          for (int j = 0; j < 32; ++j) part[(c / 2 + j) * C::RT + tid] = __uint_as_float(o[j]);
         }
       }
       tc_fence_before();
-      if (hf == 0) {
-        if (!whole) {
-          part[D * C::R] = m;
-          part[(D + 1) * C::R] = l;
-        } else if (there && p.lse != nullptr) {
-          p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int r = quadrant * 32 + hf * 16 + (lane >> 2) + 8 * k;
+          if (!whole) {
+            part[D * C::R + r] = m[k];
+            part[(D + 1) * C::R + r] = l[k];
+          } else if (there[k] && p.lse != nullptr) {
+            p.lse[at[k]] = l[k] == 0.0f ? -INFINITY : (m[k] + log2f(l[k])) * 0.6931471805599453f;
+          }
         }
       }
-      meet(false);                                              // `half` is free for the next item
+      __syncwarp();
     }
   } else if (warp < kCopyWarp) {
     // ------------------------------------------------------------ packed tiles to operands
@@ -753,10 +799,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       tc_fence_after();
       if (lane == 0) {
         const uint32_t a = tmem + buf * BT, o = tmem + C::O_COL, vb = desc_lo(smem_u32(sh.v[st][0]), BT * 128);
-        // the weights of a tile's halves stand at the begin of their halves of S
 #pragma unroll
-        for (int k = 0; k < BT / 16; ++k)
-          mma_ts<kSw128>(o, a + (k < BT / 32 ? k * 8 : BT / 2 + (k - BT / 32) * 8), vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
+        for (int k = 0; k < BT / 16; ++k) mma_ts<kSw128>(o, a + k * 8, vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
         tc_commit(&sh.pvdone[buf]);
         tc_commit(&sh.vempty[st]);
       }
@@ -822,42 +866,49 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     if (!sh.last[it]) continue;
     const Segment sg = sh.ends[it];
     const int f0 = cta_of(sg.id), parts = cta_of(sg.id + sg.tiles - 1) - f0 + 1;
-    // four threads a row, a quarter of the columns each
-    const int r = tid & 127, quarter = tid >> 7;
-    if (quarter >= 4) continue;
-    const int row = sg.rt * C::R + r;
-    if (row >= sg.rows * p.group) continue;
-    const float* base = p.part + static_cast<size_t>(f0) * 2 * ((D + 2) * C::R) + r;
+    if (warp >= kRowWarps) continue;
+    // as the rows' warps hold them
+    float m[2], l[2], inv[2];
+    size_t at[2];
+    bool there[2];
+    const float* base = p.part + static_cast<size_t>(f0) * 2 * ((D + 2) * C::R);
     auto part_of = [&](int x) { return base + static_cast<size_t>(2 * x + (x == 0 ? 1 : 0)) * ((D + 2) * C::R); };
-    float m = kNothing, l = 0.0f;
-#pragma unroll 4
-    for (int x = 0; x < parts; ++x) m = fmaxf(m, part_of(x)[D * C::R]);
-#pragma unroll 4
-    for (int x = 0; x < parts; ++x) l = fmaf(ex2(part_of(x)[D * C::R] - m), part_of(x)[(D + 1) * C::R], l);
-    const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);
-    const size_t at = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
-    constexpr int kCols = D / 4 < 32 ? D / 4 : 32;
-#pragma unroll 1
-    for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += kCols) {
-      float o[kCols];
+    const int r0 = (warp & 3) * 32 + (warp >> 2) * 16 + (lane >> 2);
 #pragma unroll
-      for (int j = 0; j < kCols; ++j) o[j] = 0.0f;
-#pragma unroll 2
+    for (int k = 0; k < 2; ++k) {
+      const int r = r0 + 8 * k, row = sg.rt * C::R + r;
+      there[k] = row < sg.rows * p.group;
+      at[k] = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
+      m[k] = kNothing;
+      l[k] = 0.0f;
+#pragma unroll 4
+      for (int x = 0; x < parts; ++x) m[k] = fmaxf(m[k], part_of(x)[D * C::R + r]);
+#pragma unroll 4
+      for (int x = 0; x < parts; ++x) l[k] = fmaf(ex2(part_of(x)[D * C::R + r] - m[k]), part_of(x)[(D + 1) * C::R + r], l[k]);
+      inv[k] = l[k] > 0.0f ? 1.0f / l[k] : (l[k] == 0.0f ? 0.0f : l[k]);
+    }
+#pragma unroll 1
+    for (int c = 0; c < D; c += 64) {
+      float o[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+#pragma unroll 1
       for (int x = 0; x < parts; ++x) {
         const float* f = part_of(x);
-        const float w = ex2(f[D * C::R] - m);
+        const float w[2] = {ex2(f[D * C::R + r0] - m[0]), ex2(f[D * C::R + r0 + 8] - m[1])};
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) o[j] = fmaf(w, f[(c + j) * C::R], o[j]);
+        for (int j = 0; j < 32; ++j) o[j] = fmaf(w[(j >> 1) & 1], f[(c / 2 + j) * C::RT + tid], o[j]);
       }
 #pragma unroll
-      for (int w = 0; w < kCols / 8; ++w) {
-        float y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = o[8 * w + e];
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + at * D)[c / 8 + w] = out_word(y, inv, p.bf16);
+      for (int j = 0; j < 32; j += 2) {
+        const int k = (j >> 1) & 1;
+        write_word(static_cast<uint16_t*>(p.out) + at[k] * D, (c >> 3) + (j >> 2), o[j] * inv[k], o[j + 1] * inv[k], p.bf16, there[k], lane);
       }
     }
-    if (p.lse != nullptr && quarter == 0) p.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+    if (p.lse != nullptr && (lane & 3) == 0)
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        if (there[k]) p.lse[at[k]] = l[k] == 0.0f ? -INFINITY : (m[k] + log2f(l[k])) * 0.6931471805599453f;
   }
 }
 
