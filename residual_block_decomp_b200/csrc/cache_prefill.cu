@@ -866,46 +866,70 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     if (!sh.last[it]) continue;
     const Segment sg = sh.ends[it];
     const int f0 = cta_of(sg.id), parts = cta_of(sg.id + sg.tiles - 1) - f0 + 1;
-    if (warp >= kRowWarps) continue;
-    // as the rows' warps hold them
-    float m[2], l[2], inv[2];
-    size_t at[2];
-    bool there[2];
+    if (tid >= 512) continue;
+    // As the rows' warps hold them, two threads a place: `half` of its columns each.  Loads of two parts are in flight
+    // together, with the weights they need.
+    const int place = tid & 255, half = tid >> 8;
     const float* base = p.part + static_cast<size_t>(f0) * 2 * ((D + 2) * C::R);
     auto part_of = [&](int x) { return base + static_cast<size_t>(2 * x + (x == 0 ? 1 : 0)) * ((D + 2) * C::R); };
-    const int r0 = (warp & 3) * 32 + (warp >> 2) * 16 + (lane >> 2);
+    const int r0 = ((place >> 5) & 3) * 32 + (place >> 7) * 16 + (lane >> 2);
+    float m[2] = {kNothing, kNothing}, l[2] = {0.0f, 0.0f}, inv[2];
+#pragma unroll 1
+    for (int x = 0; x < parts; x += 2) {
+      float pm[2][2], pl[2][2];
+#pragma unroll
+      for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const bool in = x + y < parts;
+          pm[y][k] = in ? part_of(x + y)[D * C::R + r0 + 8 * k] : kNothing;
+          pl[y][k] = in ? part_of(x + y)[(D + 1) * C::R + r0 + 8 * k] : 0.0f;
+        }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float mn = fmaxf(m[k], fmaxf(pm[0][k], pm[1][k]));
+        l[k] = l[k] * ex2(m[k] - mn) + ex2(pm[0][k] - mn) * pl[0][k] + ex2(pm[1][k] - mn) * pl[1][k];
+        m[k] = mn;
+      }
+    }
+    size_t at[2];
+    bool there[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int r = r0 + 8 * k, row = sg.rt * C::R + r;
+      const int row = sg.rt * C::R + r0 + 8 * k;
       there[k] = row < sg.rows * p.group;
       at[k] = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
-      m[k] = kNothing;
-      l[k] = 0.0f;
-#pragma unroll 4
-      for (int x = 0; x < parts; ++x) m[k] = fmaxf(m[k], part_of(x)[D * C::R + r]);
-#pragma unroll 4
-      for (int x = 0; x < parts; ++x) l[k] = fmaf(ex2(part_of(x)[D * C::R + r] - m[k]), part_of(x)[(D + 1) * C::R + r], l[k]);
       inv[k] = l[k] > 0.0f ? 1.0f / l[k] : (l[k] == 0.0f ? 0.0f : l[k]);
     }
 #pragma unroll 1
-    for (int c = 0; c < D; c += 64) {
-      float o[32];
+    for (int c = half * (D / 4); c < (half + 1) * (D / 4); c += 16) {   // of the place's D / 2 numbers
+      float o[16];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] = 0.0f;
+      for (int j = 0; j < 16; ++j) o[j] = 0.0f;
 #pragma unroll 1
-      for (int x = 0; x < parts; ++x) {
-        const float* f = part_of(x);
-        const float w[2] = {ex2(f[D * C::R + r0] - m[0]), ex2(f[D * C::R + r0 + 8] - m[1])};
+      for (int x = 0; x < parts; x += 2) {
+        const float *fa = part_of(x), *fb = part_of(x + 1 < parts ? x + 1 : x);
+        float va[16], vb[16], wa[2], wb[2];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) o[j] = fmaf(w[(j >> 1) & 1], f[(c / 2 + j) * C::RT + tid], o[j]);
+        for (int j = 0; j < 16; ++j) {
+          va[j] = fa[(c + j) * C::RT + place];
+          vb[j] = fb[(c + j) * C::RT + place];
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          wa[k] = ex2(fa[D * C::R + r0 + 8 * k] - m[k]);
+          wb[k] = x + 1 < parts ? ex2(fb[D * C::R + r0 + 8 * k] - m[k]) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = fmaf(wb[(j >> 1) & 1], vb[j], fmaf(wa[(j >> 1) & 1], va[j], o[j]));
       }
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
+      for (int j = 0; j < 16; j += 2) {
         const int k = (j >> 1) & 1;
-        write_word(static_cast<uint16_t*>(p.out) + at[k] * D, (c >> 3) + (j >> 2), o[j] * inv[k], o[j + 1] * inv[k], p.bf16, there[k], lane);
+        write_word(static_cast<uint16_t*>(p.out) + at[k] * D, (c + j) >> 2, o[j] * inv[k], o[j + 1] * inv[k], p.bf16, there[k], lane);
       }
     }
-    if (p.lse != nullptr && (lane & 3) == 0)
+    if (p.lse != nullptr && (lane & 3) == 0 && half == 0)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         if (there[k]) p.lse[at[k]] = l[k] == 0.0f ? -INFINITY : (m[k] + log2f(l[k])) * 0.6931471805599453f;
