@@ -90,7 +90,8 @@ struct CacheAttnWs {
   size_t cnt, part, frag, total;
 };
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms);
-bool cache_attn_many(int dim, int rows, int n_seqs);   // whether `rows` query rows a head run on the kernel for many
+// Whether `rows` query rows a key/value head (at most) run on the kernel for many rows.
+bool cache_attn_many(int dim, int rows, int n_seqs, int heads, int sms);
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream);
 // The kernel for many rows (cache_prefill.cu).
 size_t cache_prefill_smem(int dim, int n_seqs);

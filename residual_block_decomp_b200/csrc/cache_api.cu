@@ -169,7 +169,7 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
   const bs_status s = check_step(cache, step);
   if (s != BS_OK) return s;
   if ((dt != BS_F16 && dt != BS_BF16) || q_heads <= 0 || q_heads % cache->heads != 0 || window < 0 ||
-      !std::isfinite(scale))
+      !std::isfinite(scale * 1.4426950408889634f))
     return BS_ERR_INVALID_ARG;
   if (step->n_tokens == 0) return BS_OK;
   if (q == nullptr || out == nullptr || q_token_stride < 0 || q_head_stride < 0) return BS_ERR_INVALID_ARG;

@@ -938,8 +938,15 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
 }
 }  // namespace
 
-// Rows of a head from which the kernel for many rows is the faster one.
-bool cache_attn_many(int dim, int rows, int n_seqs) { return rows > 32 && cache_prefill_smem(dim, n_seqs) <= 227 * 1024; }
+// The kernel for few rows unpacks a context once for 16 rows (8 at D = 256), the one for many once for 128, but with a
+// tile's dozen hand-overs and larger parts to join where an item is split.  So the border is lower where there are
+// items for half the SMs and few are split.  Measured, us (few / many): 8 sequences of 4096, 4 heads, D = 128: 64 rows
+// 38 / 48, 96 rows 50 / 50, 128 rows 62 / 52; 1 of 30000: 96 rows 47 / 67, 192 rows 79 / 88; 32 of 4000: 48 rows
+// 85 / 78, 64 rows 110 / 79; D = 256, 8 of 4096: 64 rows 84 / 80, 96 rows 119 / 82.
+bool cache_attn_many(int dim, int rows, int n_seqs, int heads, int sms) {
+  const bool spread = static_cast<long long>(n_seqs) * heads * 2 >= sms;
+  return rows > (spread ? 48 : dim == 256 ? 64 : 96) && cache_prefill_smem(dim, n_seqs) <= 227 * 1024;
+}
 
 CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   CacheAttnWs w{};
@@ -951,7 +958,7 @@ CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   w.frag = w.part + static_cast<size_t>(sms) * 2 * result;
   w.total = w.frag + sms * warps * result;
   // the kernel for many rows has larger parts and no others
-  if (cache_attn_many(dim, rows, 1)) {
+  if (rows > 48) {
     const size_t many = w.part + static_cast<size_t>(sms) * 2 * cache_prefill_part_floats(dim) * 4;
     if (many > w.total) w.total = many;
   }
@@ -961,7 +968,7 @@ CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
 // Rows of an item: 8, or 16 where a head has more than 8 (the packed bytes are then
 // unpacked half as often); D = 256 keeps 8, whose accumulators are 64 registers already.
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream) {
-  if (cache_attn_many(dim, rows, p.st.n_seqs)) return launch_cache_prefill(p, dim, stream);
+  if (cache_attn_many(dim, rows, p.st.n_seqs, p.st.heads, p.grid)) return launch_cache_prefill(p, dim, stream);
   if (dim == 64) return rows > 8 ? launch_as<64, 2>(p, stream) : launch_as<64, 1>(p, stream);
   if (dim == 128) return rows > 8 ? launch_as<128, 2>(p, stream) : launch_as<128, 1>(p, stream);
   return launch_as<256, 1>(p, stream);

@@ -222,15 +222,109 @@ def test_windows_and_several_new_tokens(page, window):
 
 
 @pytest.mark.parametrize("dim,group", [(64, 4), (128, 1), (128, 4), (256, 3)])
-def test_chunks_of_a_prompt(dim, group):
-    seqs = [(0, 130), (77, 61), (300, 1)]
-    c = Case(seqs, heads=2, dim=dim, page=32, seed=dim)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_chunks_of_a_prompt(dim, group, dtype):
+    """Up to 520 query rows a head: several row tiles, the last one ragged, contexts split between CTAs."""
+    seqs = [(0, 130), (77, 61), (300, 1), (-1, 5), (0, 0), (513, 40)]
+    c = Case(seqs, heads=2, dim=dim, page=32, seed=dim, spare_rows=3)
     c.fill()
-    q = c.numbers(c.rows, 2 * group, torch.float16)
+    q = c.numbers(c.rows, 2 * group, dtype)
     out, lse = c.attend(q)
-    check_attention(c, q, out, lse, sample=24)
-    out2, lse2 = c.attend(q, 50)
-    check_attention(c, q, out2, lse2, 50, sample=24)
+    check_attention(c, q, out, lse, sample=20)
+    again, lse2 = c.attend(q)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_OK
+    c.close()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("window", [1, 20, 100, 1000])
+def test_chunks_under_a_window(dim, window):
+    seqs = [(0, 70), (300, 90), (1500, 33)]
+    c = Case(seqs, heads=1, dim=dim, page=16, seed=window)
+    c.fill(torch.bfloat16)
+    q = c.numbers(c.rows, 4, torch.bfloat16)
+    out, lse = c.attend(q, window, -0.07)
+    check_attention(c, q, out, lse, window, -0.07, sample=16)
+    c.close()
+
+
+@pytest.mark.parametrize("dim,rows", [(64, 40), (128, 24), (128, 25), (256, 17)])
+def test_borders_of_the_row_counts(dim, rows):
+    """Rows of a head around the choice of the kernel, with many sequences and with one."""
+    for n in (1, 40):
+        c = Case([(50 * i, rows) for i in range(n)] if n > 1 else [(700, rows)], heads=2, dim=dim, page=64, seed=rows)
+        c.fill()
+        q = c.numbers(c.rows, 8, torch.float16)
+        out, lse = c.attend(q)
+        check_attention(c, q, out, lse, sample=1 if n > 1 else 6)
+        c.close()
+
+
+def test_many_rows_over_one_long_context():
+    """One item's tiles on all SMs: parts of 128 rows joined, few of the rows there."""
+    c = Case([(9000, 60)], heads=1, dim=128, page=64, seed=3)
+    c.fill()
+    q = c.numbers(60, 2, torch.float16, 1.5)
+    out, lse = c.attend(q)
+    check_attention(c, q, out, lse, sample=5)
+    c.close()
+
+
+def test_many_rows_with_bad_pages_nan_and_peaked_scores():
+    c = Case([(200, 60), (64, 40)], heads=2, dim=128, page=16, seed=31)
+    c.fill()
+    q = c.numbers(c.rows, 8, torch.bfloat16, 30.0)
+    q[7, 3, 100] = float("nan")
+    q[70, 0, 0] = float("inf")
+    clean = q.clone()
+    clean[7, 3, 100] = clean[70, 0, 0] = 1.0
+    want, _ = c.attend(clean)
+    out, lse = c.attend(q)
+    bad = torch.zeros(c.rows, 8, dtype=torch.bool, device="cuda")
+    bad[7, 3] = bad[70, 0] = True
+    assert torch.equal(out[~bad], want[~bad]) and out[bad].isnan().all() and lse[bad].isnan().all()
+    check_attention(c, clean, *c.attend(clean), sample=10)
+    c.table[0, 3], c.table[0, 15], c.table[1, 0] = c.n_pages, -2, 1 << 20
+    c.step = c.make_step()
+    out, lse = c.attend(clean)
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE
+    check_attention(c, clean, out, lse, sample=10)
+    c.table[1] = -1
+    c.step = c.make_step()
+    out, lse = c.attend(clean)
+    assert (out[60:] == 0).all() and (lse[60:] == -np.inf).all()
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE
+    c.close()
+
+
+def test_prompt_pieces_in_a_graph():
+    """Append and attention of 64-token pieces captured once and replayed along a prompt."""
+    c = Case([(0, 64), (0, 40)], heads=2, dim=64, page=32, seed=32, pages_more=40)
+    own = list(range(c.n_pages))
+    c.table = np.stack([own[:12], own[12:24]]).astype(np.int32)
+    c.step = c.make_step()
+    k, v, q = (c.numbers(c.rows, h, torch.float16) for h in (2, 2, 8))
+    out, lse = torch.empty_like(q), torch.empty(c.rows, 8, device="cuda")
+    ws = torch.zeros(R.bs_cache_attention_workspace_bytes(c.handle, c.step, 8), dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        R.bs_cache_append(c.handle, c.step, k, v)
+        R.bs_cache_attention(c.handle, c.step, q, out, ws, lse=lse)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        R.bs_cache_append(c.handle, c.step, k, v)
+        R.bs_cache_attention(c.handle, c.step, q, out, ws, lse=lse)
+    for _ in range(4):
+        for x in (k, v, q):
+            x.copy_(torch.from_numpy(c.gen.standard_normal(x.shape).astype(np.float32)))
+        g.replay()
+        torch.cuda.synchronize()
+        check_attention(c, q, out, lse, sample=8)
+        c.start = (c.start + [64, 40]).astype(np.int32)
+        c.step.start.copy_(torch.from_numpy(c.start))
     c.close()
 
 
