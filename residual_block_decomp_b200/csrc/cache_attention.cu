@@ -28,7 +28,10 @@
 //  * Softmax: the accumulator layout holds rows = tokens, columns = query rows.  The reference m of the weights
 //    2^(x - m) follows the running maximum only when a score passes it by more than 8 (weights stay below 2^8,
 //    far inside fp16): most tiles then need no shuffles and no rescaling, only a vote.
-//    movmatrix turns the fp16 weights into the next product's B fragment.
+//    movmatrix turns the fp16 weights into the next product's B fragment.  Rows that are fp16 themselves take the
+//    weights in two fp16 parts: one rounding of the weights and that of the values together moved an fp16 result by
+//    1.5 times what its own rounding does, the values' alone move it by 1.25 times.  A bf16 result is rounded by 8 times
+//    as much, and one part is enough.
 //  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
 //    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).
 //    Scales cannot stay outside the product here as for keys: the token is what is summed over.
@@ -58,10 +61,8 @@ struct Cfg {
   static constexpr int R = 8 * NT;                            // query rows of an item
   static constexpr int OREG = NT * J * 16;                    // accumulators of a lane
   static constexpr int FREG = OREG + 4 * NT;                  // and its maxima and sums
-  static constexpr int FBYTES = FREG * 128;                   // a warp's partial result
   static constexpr int NW = (NT == 1 && D <= 128) ? kWarps : 8;   // warps
   static constexpr int ST = 2;                                // stages of a warp
-  static constexpr int UC = chunk_bytes(D) / 16;              // 16-byte units of a chunk
 };
 
 // Partial results are laid out [register][lane].
@@ -394,6 +395,8 @@ struct State {
   }
 
   // One tile: positions pos0 .., of which `ok` chunks hold tokens; `masked`: some (row, token) is hidden.
+  // FINE: weights in two fp16 parts.
+  template <bool FINE>
   __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int end, uint32_t ok, bool masked, int window, int lane) {
     const int t = lane >> 2, cc = lane & 3;
     if (pos0 + C::TILE > end) {
@@ -508,13 +511,20 @@ struct State {
         for (int e = 0; e < 4; ++e) s[mt][nt][e] = ex2(fmaf(s[mt][nt][e], q.factor[nt][e & 1], -m[nt][e & 1]));
 #pragma unroll
     for (int mt = 0; mt < C::TM; ++mt) {
-      uint32_t b[NT][2];
+      uint32_t b[NT][2], lo[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         l[nt][0] += s[mt][nt][0] + s[mt][nt][2];
         l[nt][1] += s[mt][nt][1] + s[mt][nt][3];
-        b[nt][0] = movmatrix(h2u(__floats2half2_rn(s[mt][nt][0], s[mt][nt][1])));
-        b[nt][1] = movmatrix(h2u(__floats2half2_rn(s[mt][nt][2], s[mt][nt][3])));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const __half2 hi = __floats2half2_rn(s[mt][nt][2 * k], s[mt][nt][2 * k + 1]);
+          b[nt][k] = movmatrix(h2u(hi));
+          if (FINE) {
+            const float2 f = __half22float2(hi);
+            lo[nt][k] = movmatrix(h2u(__floats2half2_rn(s[mt][nt][2 * k] - f.x, s[mt][nt][2 * k + 1] - f.y)));
+          }
+        }
       }
       // the lane's tokens 2 cc, 2 cc + 1, 2 cc + 8, 2 cc + 9: rows cc, cc + 8, cc + 4, cc + 12
       const uint8_t* ch = st + mt * chunk_bytes(D) + 10 * D;
@@ -544,7 +554,10 @@ struct State {
           const uint32_t a0 = h2u(__hfma2(c0, sx, bx)), a1 = h2u(__hfma2(c1, sx, bx));
           const uint32_t a2 = h2u(__hfma2(c2, sy, by)), a3 = h2u(__hfma2(c3, sy, by));
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][j][e], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816(o[nt][j][e], a0, a1, a2, a3, b[nt][0], b[nt][1]);
+            if (FINE) mma16816(o[nt][j][e], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
+          }
         }
       }
     }
@@ -665,7 +678,7 @@ __device__ __forceinline__ void store_joined(float* f, int nt, int j, const Join
   if (j == 0) to[(C::OREG / 4 + nt) * 32] = r.ml;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FINE>
 __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel(const __grid_constant__ CacheAttnParams p) {
   using C = Cfg<D, NT>;
   extern __shared__ __align__(16) uint8_t raw[];
@@ -777,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
       const int pos0 = c.first + c.t * C::TILE;
       const uint32_t ok = have & ((1u << C::TM) - 1);
       const bool masked = ok != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest || pos0 <= q.highest - p.window;
-      st.tile(q, sh.stage[warp][slot], pos0, c.end, ok, masked, p.window, lane);
+      st.template tile<FINE>(q, sh.stage[warp][slot], pos0, c.end, ok, masked, p.window, lane);
       __syncwarp();
       ask(slot);
       slot = slot + 1 == C::ST ? 0 : slot + 1;
@@ -919,7 +932,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
   }
 }
 
-template <int D, int NT>
+template <int D, int NT, bool FINE>
 cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
   constexpr int kMost = static_cast<int>(sizeof(Shared<D, NT>) + (kCacheMaxSeqs + 1) * 8);
   // the attribute is the device's: set it once for each (up to 64 devices; every call beyond)
@@ -929,12 +942,16 @@ cudaError_t launch_as(const CacheAttnParams& p, cudaStream_t stream) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (bit == 0 || !(set.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(cache_attention_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    e = cudaFuncSetAttribute(cache_attention_kernel<D, NT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
     if (e != cudaSuccess) return e;
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const size_t smem = sizeof(Shared<D, NT>) + (static_cast<size_t>(p.st.n_seqs) + 1) * 8;
-  return launch_chained(cache_attention_kernel<D, NT>, dim3(p.grid), Cfg<D, NT>::NW * 32, smem, stream, p);
+  return launch_chained(cache_attention_kernel<D, NT, FINE>, dim3(p.grid), Cfg<D, NT>::NW * 32, smem, stream, p);
+}
+template <int D, int NT>
+cudaError_t launch_type(const CacheAttnParams& p, cudaStream_t stream) {
+  return p.bf16 ? launch_as<D, NT, false>(p, stream) : launch_as<D, NT, true>(p, stream);
 }
 }  // namespace
 
@@ -969,9 +986,9 @@ CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
 // unpacked half as often); D = 256 keeps 8, whose accumulators are 64 registers already.
 cudaError_t launch_cache_attention(const CacheAttnParams& p, int dim, int rows, cudaStream_t stream) {
   if (cache_attn_many(dim, rows, p.st.n_seqs, p.st.heads, p.grid)) return launch_cache_prefill(p, dim, stream);
-  if (dim == 64) return rows > 8 ? launch_as<64, 2>(p, stream) : launch_as<64, 1>(p, stream);
-  if (dim == 128) return rows > 8 ? launch_as<128, 2>(p, stream) : launch_as<128, 1>(p, stream);
-  return launch_as<256, 1>(p, stream);
+  if (dim == 64) return rows > 8 ? launch_type<64, 2>(p, stream) : launch_type<64, 1>(p, stream);
+  if (dim == 128) return rows > 8 ? launch_type<128, 2>(p, stream) : launch_type<128, 1>(p, stream);
+  return launch_type<256, 1>(p, stream);
 }
 
 }  // namespace bs

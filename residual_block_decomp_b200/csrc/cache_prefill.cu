@@ -6,7 +6,7 @@
 // 128 query rows), its context is taken in tiles of 128 tokens (D = 256: 64), and a tile's packed bytes are expanded
 // once in shared memory for all rows.  Per tile
 //     S = Q K^T             (Q and S in tensor memory, K in shared memory, fp32 sums)
-//     P = 2^(S f - m)       as fp16, written over S in tensor memory
+//     P = 2^(S f - m)       as fp16 (two parts for fp16 rows, as in the kernel for few), over S in tensor memory
 //     O += P V              (P and O in tensor memory, V in shared memory with the dims contiguous)
 // with the maximum and sum of a row in registers.  As in the kernel for few rows the reference m follows the maximum
 // only when a score passes it by 8 (weights up to 2^8), so O is hardly ever rescaled.
@@ -578,8 +578,20 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
             l[1] += d + e;
             pr[j / 2] = h2u(__floats2half2_rn(a, b));
             pr[j / 2 + 1] = h2u(__floats2half2_rn(d, e));
+            x[j] = __float_as_uint(a);
+            x[j + 1] = __float_as_uint(b);
+            x[j + 2] = __float_as_uint(d);
+            x[j + 3] = __float_as_uint(e);
           }
-          tmem_st_pairs(s_at + c / 2, pr);                      // over scores of these rows that have been read
+          tmem_st_pairs(s_at + c, pr);                          // over scores of these rows that have been read
+          if (!p.bf16) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 h = __half22float2(u2h(pr[j / 2]));   // registers (j, j + 1) of both arrays are the same pair
+              pr[j / 2] = h2u(__floats2half2_rn(__uint_as_float(x[j]) - h.x, __uint_as_float(x[j + 1]) - h.y));
+            }
+            tmem_st_pairs(s_at + c + 32, pr);
+          }
         }
         tc_wait_st();
         tc_fence_before();
@@ -800,7 +812,12 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       if (lane == 0) {
         const uint32_t a = tmem + buf * BT, o = tmem + C::O_COL, vb = desc_lo(smem_u32(sh.v[st][0]), BT * 128);
 #pragma unroll
-        for (int k = 0; k < BT / 16; ++k) mma_ts<kSw128>(o, a + k * 8, vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
+        for (int k = 0; k < BT / 16; ++k)
+          mma_ts<kSw128>(o, a + (k >> 2) * 64 + (k & 3) * 8, vb + k * (2048 >> 4), kIdO, begin && k == 0 ? 0u : 1u);
+        if (!p.bf16) {
+#pragma unroll
+          for (int k = 0; k < BT / 16; ++k) mma_ts<kSw128>(o, a + (k >> 2) * 64 + 32 + (k & 3) * 8, vb + k * (2048 >> 4), kIdO, 1u);
+        }
         tc_commit(&sh.pvdone[buf]);
         tc_commit(&sh.vempty[st]);
       }
