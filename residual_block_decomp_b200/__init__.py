@@ -21,7 +21,7 @@ _BINDING_NAMES = (
     "CacheStep", "bs_cache_append", "bs_cache_attention", "bs_cache_attention_workspace_bytes", "bs_cache_create",
     "bs_cache_destroy", "bs_cache_device_bytes", "bs_cache_get_device_error", "bs_cache_page_bytes", "bs_cache_read",
 )
-_LAYER_NAMES = ("BitStackLinear",)
+_LAYER_NAMES = ("BitStackAttention", "BitStackCache", "BitStackLinear", "PageTable")
 __all__ = list(_BINDING_NAMES) + list(_LAYER_NAMES)
 
 

@@ -30,7 +30,8 @@
 //    far inside fp16): most tiles then need no shuffles and no rescaling, only a vote.
 //    movmatrix turns the fp16 weights into the next product's B fragment.  Rows that are fp16 themselves take the
 //    weights in two fp16 parts: one rounding of the weights and that of the values together moved an fp16 result by
-//    1.5 times what its own rounding does, the values' alone move it by 1.25 times.  A bf16 result is rounded by 8 times
+//    1.5 times what its own rounding does, the values' alone move it by 1.3 to 1.4 times (4 sequences of 128K: 144 ->
+//    155 us).  A bf16 result is rounded by 8 times
 //    as much, and one part is enough.
 //  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
 //    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).

@@ -225,3 +225,39 @@ def test_lane_reads_hit_their_numbers(dim):
                 base = 10 * dim + (row * 128 + (t ^ ((row & 3) << 1)) * 16 if dim == 256 else row * (dim // 2) + t * (dim // 16))
                 assert (at(base + 4 * j), 0) == oc.code_place(dim, True, tok, 8 * w)
                 assert at(18 * dim + row * (dim // 8) + (t >> 2) * (dim // 16) + 4 * j) == oc.pair_place(dim, True, tok, w // 4)
+
+
+# ------------------------------------------------------------------- page table ---
+def test_page_table_hands_out_each_page_once_and_takes_them_back():
+    t = R.PageTable(10, 16)
+    a, b = t.open(), t.open()
+    start, pages = t.advance([a, b], [16, 17])
+    assert start == [0, 0] and [len(p) for p in pages] == [1, 2]
+    start, pages = t.advance([b, a], [15, 0])
+    assert start == [17, 16] and [len(p) for p in pages] == [2, 1]
+    start, pages = t.advance([a], [1], room=40)      # 17 tokens, pages for 57
+    assert start == [16] and len(pages[0]) == 4 and t.length[a] == 17
+    assert t.advance([a], [40])[0] == [17] and len(t.pages[a]) == 4
+    held = t.pages[a] + t.pages[b]
+    assert len(set(held + t.free)) == 10 and len(held + t.free) == 10
+    mine = list(t.pages[a])
+    t.close(a)
+    c = t.open()
+    assert c not in (a, b) and t.advance([c], [64])[1][0] == mine
+
+
+def test_page_table_refusals_change_nothing():
+    t = R.PageTable(4, 32)
+    a, b = t.open(), t.open()
+    t.advance([a], [33])
+    before = (dict(t.length), {k: list(v) for k, v in t.pages.items()}, list(t.free))
+    for seqs, new, room, error in [([a, a], [1, 1], 0, ValueError), ([a], [1, 2], 0, ValueError), ([], [], 0, ValueError),
+                                   ([a], [-1], 0, ValueError), ([a], [1], -1, ValueError), ([a, 9], [1, 1], 0, KeyError),
+                                   ([a, b], [32, 64], 0, R.BsError), ([b], [1], 100, R.BsError),
+                                   ([a], [2 ** 31 - 33], 0, R.BsError)]:
+        with pytest.raises(error):
+            t.advance(seqs, new, room)
+        assert before == (dict(t.length), {k: list(v) for k, v in t.pages.items()}, list(t.free))
+    t.advance([a, b], [31, 64])
+    with pytest.raises(KeyError):
+        t.close(17)
