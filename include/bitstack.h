@@ -455,16 +455,23 @@ size_t bs_cache_attention_workspace_bytes(bs_cache_t cache, const bs_cache_step*
  * the same dtype, 16-byte aligned; lse (may be NULL) [n_tokens][q_heads] fp32 gets
  * ln sum_t exp(scale q . k_t), with which results over disjoint contexts are joined.
  * A row that sees nothing (an empty slot, all its pages outside the pool) gets 0 and
- * -inf.  Scores, the softmax's maximum and sum and the accumulated output are fp32;
- * the weights exp(s - max) and the dequantised values enter the product in fp16 (half a
- * step of fp16 each).  Results do not depend on timing: the same step gives the same
- * bits.  Asynchronous on `stream`; capturable; the current device must be the cache's. */
+ * -inf; a row of q with an infinity or a NaN gets NaN, and no other row does.
+ * Scores, the softmax's maximum and sum and the accumulated output are fp32; the
+ * dequantised values enter the product in fp16 (half a step), and so do the weights
+ * exp(s - max) of BF16 rows (those of F16 rows in two fp16 parts).  Results do not
+ * depend on timing: the same step gives the same bits.
+ * Few rows a head run on one kernel, many on another, whose waits are bounded
+ * (500 ms); one that runs out is reported as BS_ERR_TIMEOUT, and the workspace has to
+ * be zeroed again then.  BS_ERR_INVALID_ARG for a scale that is not finite (times
+ * log2 e, in fp32) or window < 0; BS_ERR_CAPACITY for a workspace that is too small.
+ * Asynchronous on `stream`; capturable; the current device must be the cache's. */
 bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const void* q, long long q_token_stride,
                              long long q_head_stride, int q_heads, bs_dtype dt, float scale, int window, void* out,
                              float* lse, void* workspace, size_t workspace_bytes, bs_stream_t stream);
 
 /* Synchronises the cache's device, reads and clears the pool's error word: BS_OK,
- * BS_ERR_RANGE (a step named rows, positions or pages outside their bounds), or BS_ERR_CUDA. */
+ * BS_ERR_RANGE (a step named rows, positions or pages outside their bounds),
+ * BS_ERR_TIMEOUT (a bounded wait of bs_cache_attention ran out), or BS_ERR_CUDA. */
 bs_status bs_cache_get_device_error(bs_cache_t cache);
 
 /* ------------------------------------------------------------------ errors ----- */

@@ -31,11 +31,18 @@
 //    movmatrix turns the fp16 weights into the next product's B fragment.  Rows that are fp16 themselves take the
 //    weights in two fp16 parts: one rounding of the weights and that of the values together moved an fp16 result by
 //    1.5 times what its own rounding does, the values' alone move it by 1.3 to 1.4 times (4 sequences of 128K: 144 ->
-//    155 us).  A bf16 result is rounded by 8 times
-//    as much, and one part is enough.
+//    155 us).  A bf16 result is rounded by 8 times as much, and one part is enough.
 //  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
 //    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).
 //    Scales cannot stay outside the product here as for keys: the token is what is summed over.
+//
+// What bounds it.  A tile (5120 bytes) takes about 720 warp instructions (keys 190, values 300, softmax 70, copies and
+// the loop 160), 0.52 to 0.6 of the issue slots with three warps a scheduler; the arithmetic pipes are 33 to 44 % busy.
+// Measured: 64 sequences of up to 8K (8 heads of 128, 4 queries a head) 102 us, 0.66 of the copy rate; 4 of 128K in
+// fp16 155 us, 0.66; one of 32K 24 us; 777 tokens 12 us, 2 of them for tiles: the list, the first copy, the queries and
+// the joins are the rest.  Taken back: three stages a warp instead of two (105 us), 8, 10, 14 or 16 warps instead of
+// 12, and the keys of the next tile between the values of this one in one stretch of code (104 us; 32K 25 us): neither
+// the copies' latency nor the products' is what is waited for.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

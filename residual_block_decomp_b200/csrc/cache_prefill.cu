@@ -26,7 +26,10 @@
 // What was measured on the way (2 sequences of 512 new tokens over 4K, 4 heads a key head): two groups of 128 rows with
 // Q in shared memory, 64-token products 141 us, 128-token products 128 us: an operand in shared memory is read at 128
 // bytes a clock, and Q and K together take the products' whole time (or more, at 64 tokens) for it.  Q in tensor memory
-// halves that, and leaves room for two buffers of S with one group.
+// halves that, and leaves room for two buffers of S with one group: 111 us; rows held by four neighbouring lanes instead
+// of two warps that meet 101; parts of split items joined by 16 warps 96.  What bounds it now: about 232 KB through
+// shared memory a tile of 128 x 128 (expanded keys 64, values 32, written once and read once, packed bytes 20 twice),
+// 1.8 thousand of its 2.9 thousand cycles, with the expansion's and the softmax's instructions beside it.
 //
 // 8 numbers of a word are kept in the order (0, 4, 1, 5, 2, 6, 3, 7) that unpacking gives, in Q and K alike (a sum
 // does not mind), and in V as the order of O's columns, undone where rows are written.
