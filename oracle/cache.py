@@ -112,7 +112,7 @@ def spans(n_seqs, n_tokens, max_new, cu, start, table_width, page_tokens):
         bad = lo < 0 or hi < lo or hi > n_tokens
         rows = 0 if bad else hi - lo
         live = not bad and start[i] >= 0 and rows > 0
-        if live and (rows > max_new or int(start[i]) + rows > table_width * page_tokens):
+        if live and (rows > max_new or int(start[i]) + rows > min(table_width * page_tokens, 2 ** 31 - 512)):
             live, bad = False, True
         out.append((lo, rows, int(start[i]), live, bad))
     return out

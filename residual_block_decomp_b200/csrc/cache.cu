@@ -49,7 +49,7 @@ template <>
 struct Eight<__half> {
   uint4 a;
   __device__ bool beyond() const { return reaches(a, 0x7bf0u); }   // the first fp16 number above 65000, inf, NaN
-  __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void load(const void* p) { a = *static_cast<const uint4*>(p); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -73,7 +73,7 @@ template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
   __device__ bool beyond() const { return reaches(a, 0x477eu); }   // the first bf16 number above 65000, inf, NaN
-  __device__ void load(const void* p) { a = __ldg(static_cast<const uint4*>(p)); }
+  __device__ void load(const void* p) { a = *static_cast<const uint4*>(p); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -102,8 +102,8 @@ struct Eight<float> {
     return m > kCacheClamp || sum != sum;
   }
   __device__ void load(const void* p) {
-    a = __ldg(static_cast<const float4*>(p));
-    b = __ldg(static_cast<const float4*>(p) + 1);
+    a = *static_cast<const float4*>(p);
+    b = static_cast<const float4*>(p)[1];
   }
   __device__ void get(float (&x)[8]) const {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       if (h < heads)
         in[e].load(static_cast<const T*>(p.in[kv]) + (s.row0 + i) * p.tok[kv] + h * p.head[kv] + u % LR * 8);
     }
-    const int page = __ldg(p.st.table + static_cast<size_t>(seq) * p.st.stride + (pos >> p.st.page_shift));
+    const int page = p.st.table[static_cast<size_t>(seq) * p.st.stride + (pos >> p.st.page_shift)];
     uint8_t* ch = chunk_at(p.st, page, pos, h0, D);
     if (ch == nullptr) {
       if (lane == 0) atomicOr(p.st.err, kErrRange);
@@ -248,7 +248,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
     const int h = static_cast<int>(v % heads), pos0 = (first + static_cast<int>(v / heads)) * kChunkTokens;
     const uint8_t* ch = nullptr;
     if (s.live) {
-      const int page = __ldg(p.st.table + static_cast<size_t>(seq) * p.st.stride + (pos0 >> p.st.page_shift));
+      const int page = p.st.table[static_cast<size_t>(seq) * p.st.stride + (pos0 >> p.st.page_shift)];
       ch = chunk_at(p.st, page, pos0, h, D);
       if (ch == nullptr && lane == 0) atomicOr(p.st.err, kErrRange);
     }
@@ -262,15 +262,15 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         code[kv][i] = pair[kv][i] = make_uint4(0, 0, 0, 0);
         if (ch == nullptr || r < 0 || r >= s.rows || p.out[kv] == nullptr) continue;
         const uint8_t* base = ch + kv * 10 * D;
-        code[kv][i] = __ldg(reinterpret_cast<const uint4*>(base + u * 16));
+        code[kv][i] = *reinterpret_cast<const uint4*>(base + u * 16);
         const uint8_t* pr = base + 8 * D + row * (D / 8);
         if (kv ? J == 4 : GR >= 4) {             // four consecutive pairs
-          pair[kv][i] = __ldg(reinterpret_cast<const uint4*>(pr + (kv ? c / 4 : c % (GR < 4 ? 1 : GR / 4)) * 16));
+          pair[kv][i] = *reinterpret_cast<const uint4*>(pr + (kv ? c / 4 : c % (GR < 4 ? 1 : GR / 4)) * 16);
         } else if (kv ? J == 2 : true) {         // two, for words 0, 1 and 2, 3
-          const uint2 two = __ldg(reinterpret_cast<const uint2*>(pr + (kv ? c / 2 * 8 : 0)));
+          const uint2 two = *reinterpret_cast<const uint2*>(pr + (kv ? c / 2 * 8 : 0));
           pair[kv][i] = make_uint4(two.x, two.y, two.x, two.y);
         } else {
-          const uint32_t one = __ldg(reinterpret_cast<const uint32_t*>(pr + c * 4));
+          const uint32_t one = *reinterpret_cast<const uint32_t*>(pr + c * 4);
           pair[kv][i] = make_uint4(one, one, one, one);
         }
       }

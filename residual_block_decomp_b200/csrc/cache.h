@@ -13,11 +13,15 @@ namespace bs {
 constexpr int kChunkTokens = 16;     // tokens of a chunk: one matrix tile's rows
 constexpr int kCacheMaxSeqs = 4096;  // sequences of a step (their tile counts are prefix-summed in shared memory)
 
+constexpr int kCacheMaxPos = 0x7fffffff - 511;   // positions are below it: the end of a tile stays an int
+
 constexpr uint32_t kErrRange = 2u;   // device error word bit: a step left its bounds
 
 __host__ __device__ constexpr int chunk_bytes(int dim) { return 20 * dim; }
 
-// A step as the kernels take it (pointers to device memory).
+// A step as the kernels take it (pointers to device memory).  The kernels start while the one before them in
+// the stream may still run (launch_chained) and wait for it before they load anything: with ordinary loads, as what
+// an earlier kernel of the chain wrote is not constant over the life of a kernel that waits for it.
 struct StepParams {
   uint8_t* pages;
   unsigned long long page_bytes;
@@ -52,8 +56,8 @@ __device__ __forceinline__ SeqSpan seq_span(const StepParams& p, int i) {
   s.rows = s.bad ? 0 : static_cast<int>(hi - lo);
   s.start = start;
   s.live = !s.bad && start >= 0 && s.rows > 0;
-  if (s.live && (s.rows > p.max_new ||
-                 static_cast<long long>(start) + s.rows > (static_cast<long long>(p.width) << p.page_shift))) {
+  const long long end = static_cast<long long>(start) + s.rows;
+  if (s.live && (s.rows > p.max_new || end > (static_cast<long long>(p.width) << p.page_shift) || end > kCacheMaxPos)) {
     s.live = false;
     s.bad = true;
   }

@@ -254,7 +254,7 @@ struct Worker {
           fd.seq = c.seq;
           fd.block = idx >> 5;
           const int mine = (fd.block << 5) + lane;
-          fd.page = mine <= (c.end - 1) >> shift ? __ldg(p.st.table + static_cast<size_t>(c.seq) * p.st.stride + mine) : 0;
+          fd.page = mine <= (c.end - 1) >> shift ? p.st.table[static_cast<size_t>(c.seq) * p.st.stride + mine] : 0;
         }
         const uint32_t page = __shfl_sync(0xffffffffu, fd.page, idx & 31);
         const int in_page = (1 << shift) / kChunkTokens;
@@ -300,7 +300,7 @@ struct Rows {
       uint4 raw[C::GR];
 #pragma unroll
       for (int gr = 0; gr < C::GR; ++gr)
-        raw[gr] = row < total ? __ldg(reinterpret_cast<const uint4*>(src + gr * 32)) : make_uint4(0, 0, 0, 0);
+        raw[gr] = row < total ? *reinterpret_cast<const uint4*>(src + gr * 32) : make_uint4(0, 0, 0, 0);
       auto two = [&](uint32_t r) {   // two numbers in fp32
         return p.bf16 ? make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u)) : __half22float2(u2h(r));
       };

@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         uint32_t top = 0;
 #pragma unroll 4
         for (int w = 0; w < D / 16; ++w) {
-          const uint4 a = there ? __ldg(src + w) : make_uint4(0, 0, 0, 0);
+          const uint4 a = there ? src[w] : make_uint4(0, 0, 0, 0);
           top = __vmaxu2(__vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu)), top);
         }
         top = max(top & 0xffffu, top >> 16);
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           const int gr = hf * (C::GR / 2) + g;
           uint4 raw[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) raw[k] = there && ex != 255 ? __ldg(src + 4 * g + k) : make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < 4; ++k) raw[k] = there && ex != 255 ? src[4 * g + k] : make_uint4(0, 0, 0, 0);
           float sum = 0.0f;
           uint32_t cols[16];
 #pragma unroll
@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       auto look = [&](int t) {
         const int pos = sg.first + t * BT + lane * kChunkTokens;
         entry = lane < C::CHUNKS && pos < sg.end
-                    ? __ldg(p.st.table + static_cast<size_t>(sg.seq) * p.st.stride + (pos >> p.st.page_shift)) : -1;
+                    ? p.st.table[static_cast<size_t>(sg.seq) * p.st.stride + (pos >> p.st.page_shift)] : -1;
       };
       look(sg.t0);
       for (int t = sg.t0; t < sg.t1 && ok; ++t, ++i) {

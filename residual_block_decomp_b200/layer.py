@@ -185,7 +185,7 @@ class PageTable:
             if s not in self.length:
                 raise KeyError(f"no sequence {s}")
         start = [self.length[s] for s in seqs]
-        if max(a + n for a, n in zip(start, new)) + room > 2 ** 31 - 1:
+        if max(a + n for a, n in zip(start, new)) + room > 2 ** 31 - 512:
             raise B.BsError(B.BS_ERR_RANGE, "PageTable.advance")
         need = [max(0, -(-(a + n + room) // self.page_tokens) - len(self.pages[s])) for s, a, n in zip(seqs, start, new)]
         if sum(need) > len(self.free):

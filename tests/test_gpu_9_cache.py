@@ -582,6 +582,78 @@ def test_shared_pages_and_one_workspace_for_changing_steps():
     c.close()
 
 
+@pytest.mark.parametrize("graph", [True, False])
+def test_a_chain_of_reads_and_writes_sees_each_write(graph):
+    """read, append, read, attention of the same positions, back to back: every kernel starts while the one before it
+    ends, and none may work on what it, or one before it, held in a cache."""
+    c = Case([(0, 9), (0, 30), (0, 1)], heads=2, dim=64, page=16, seed=41)
+    k, v = c.numbers(c.rows, 2, torch.float16), c.numbers(c.rows, 2, torch.float16)
+    q = c.numbers(c.rows, 4, torch.float16)
+    new_k, new_v = torch.empty_like(k), torch.empty_like(v)
+    first, second = torch.empty((2, *k.shape), device="cuda"), torch.empty((2, *k.shape), device="cuda")
+    out = torch.empty_like(q)
+    ws = torch.zeros(R.bs_cache_attention_workspace_bytes(c.handle, c.step, 4), dtype=torch.uint8, device="cuda")
+
+    def chain():
+        R.bs_cache_append(c.handle, c.step, k, v)
+        R.bs_cache_read(c.handle, c.step, first[0], first[1])
+        R.bs_cache_append(c.handle, c.step, new_k, new_v)
+        R.bs_cache_read(c.handle, c.step, second[0], second[1])
+        R.bs_cache_attention(c.handle, c.step, q, out, ws)
+
+    if graph:
+        chain()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            chain()
+    for _ in range(30):
+        for x in (k, v, new_k, new_v):
+            x.copy_(torch.from_numpy(c.gen.standard_normal(x.shape).astype(np.float32)))
+        g.replay() if graph else chain()
+        torch.cuda.synchronize()
+        for got, dense in ((first[0], k), (first[1], v), (second[0], new_k), (second[1], new_v)):
+            codes, s, b = oc.quantise(dense.float().cpu().numpy())
+            assert np.array_equal(got.double().cpu().numpy().reshape(-1), np.float32(oc.dequantise(codes, s, b)).astype(np.float64).reshape(-1))
+        want, _ = c.attend(q)
+        assert torch.equal(out, want)
+    c.close()
+
+
+@pytest.mark.parametrize("new", [3, 60])
+def test_positions_up_to_the_largest(new):
+    """The last positions of a context of 2^31 - 512 tokens under a window, in shared pages: as the same
+    tokens at the end of a context of 512."""
+    c = Case([(512 - new, new)], heads=1, dim=64, page=256, seed=new, pages_more=1)
+    c.fill()
+    q = c.numbers(new, 2, torch.float16)
+    want = c.attend(q, 200)
+    check_attention(c, q, *want, 200, sample=8)
+    end = 2 ** 31 - 512
+    table = torch.full((1, 2 ** 23), c.n_pages + 5, dtype=torch.int32, device="cuda")
+    table[0, end // 256 - 2:end // 256] = torch.from_numpy(c.table[0, :2]).cuda()
+    start = torch.tensor([end - new], dtype=torch.int32, device="cuda")
+    far = R.CacheStep(start, table, new, new, torch.tensor([0, new], dtype=torch.int32, device="cuda"))
+    got = c.attend(q, 200, step=far)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k, v = c.numbers(new, 1, torch.float16), c.numbers(new, 1, torch.float16)
+    R.bs_cache_append(c.handle, far, k, v)
+    here, there = torch.empty((2, 2, *k.shape), dtype=torch.float16, device="cuda")
+    R.bs_cache_read(c.handle, far, there[0], there[1])
+    R.bs_cache_read(c.handle, c.step, here[0], here[1])
+    assert torch.equal(here, there) and (here[0] - k).abs().max() < 0.5
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_OK
+    start += 1
+    out, lse = c.attend(q, 200, step=far)
+    R.bs_cache_append(c.handle, far, k * 0, v * 0)
+    R.bs_cache_read(c.handle, far, there[0], there[1])
+    assert (out == 0).all() and (lse == -np.inf).all() and (there == 0).all()
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE
+    R.bs_cache_read(c.handle, c.step, there[0], there[1])
+    assert torch.equal(here, there)
+    c.close()
+
+
 def test_pages_beyond_four_gib():
     heads, dim, page = 8, 128, 64
     n_pages = (9 << 29) // R.bs_cache_page_bytes(heads, dim, page)
