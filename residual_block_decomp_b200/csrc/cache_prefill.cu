@@ -436,6 +436,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
         top = max(top & 0xffffu, top >> 16);
         sh.top[hf][r] = top;
+        uint4 raw[4];                                           // a group's numbers, loaded one group ahead
+#pragma unroll
+        for (int k = 0; k < 4; ++k) raw[k] = there ? src[k] : make_uint4(0, 0, 0, 0);
         meet();
         if (!ok) break;
         top = max(top, sh.top[hf ^ 1][r]);
@@ -451,14 +454,13 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 #pragma unroll 1
         for (int g = 0; g < C::GR / 2; ++g) {
           const int gr = hf * (C::GR / 2) + g;
-          uint4 raw[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) raw[k] = there && ex != 255 ? src[4 * g + k] : make_uint4(0, 0, 0, 0);
           float sum = 0.0f;
           uint32_t cols[16];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const uint32_t x[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+            const bool finite = ex != 255;
+            const uint32_t x[4] = {finite ? raw[k].x : 0, finite ? raw[k].y : 0, finite ? raw[k].z : 0, finite ? raw[k].w : 0};
+            if (there && g + 1 < C::GR / 2) raw[k] = src[4 * (g + 1) + k];
             uint32_t h[4];                                      // dims 2 e, 2 e + 1
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
