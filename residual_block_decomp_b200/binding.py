@@ -341,7 +341,7 @@ def bs_cache_create(heads: int, dim: int, page_tokens: int, n_pages: int, dev_pa
     st = lib.bs_cache_create(heads, dim, page_tokens, n_pages, _ptr(dev_pages),
                              dev_pages.numel() * dev_pages.element_size(), _stream(stream), ctypes.byref(h))
     _check(st, "bs_cache_create")
-    _cache_shapes[h.value] = (heads, dim, dev_pages.device)
+    _cache_shapes[h.value] = (heads, dim, dev_pages.device, dev_pages.get_device())
     return h.value
 
 
@@ -350,8 +350,8 @@ def bs_cache_destroy(handle: int) -> None:
     _cache_shapes.pop(handle, None)
 
 
-_NO_CACHE = (None, None, None)
-_cache_shapes: dict[int, tuple] = {}   # (heads, dim, device) of live handles, for the tensors' checks
+_NO_CACHE = (None, None, None, None)
+_cache_shapes: dict[int, tuple] = {}   # (heads, dim, device, its index) of live handles, for the tensors' checks
 
 
 def _ints(t, name: str, shape: tuple) -> int:
@@ -387,7 +387,7 @@ class CacheStep:
 def _rows(t, name: str, handle: int, step: CacheStep, query: bool = False) -> tuple:
     """(pointer, token stride, head stride) of a tensor [n_tokens, heads, dim] with contiguous numbers
     on the cache's GPU; a query's heads are a multiple of the cache's (checked by the library)."""
-    heads, dim, device = _cache_shapes.get(handle, _NO_CACHE)
+    heads, dim, device, _ = _cache_shapes.get(handle, _NO_CACHE)
     shape = t.shape
     if len(shape) != 3 or shape[0] != step.n_tokens or shape[2] != dim or (shape[1] != heads and not query):
         raise ValueError(f"{name}: need [{step.n_tokens}, {'q_heads' if query else heads}, {dim}], got {list(shape)}")
@@ -399,6 +399,14 @@ def _rows(t, name: str, handle: int, step: CacheStep, query: bool = False) -> tu
     return t.data_ptr(), tok, head
 
 
+def _cache_stream(handle: int, stream) -> int | None:
+    """As _stream; None is the current stream of the cache's device (which has to be current)."""
+    if stream is not None:
+        return _stream(stream)
+    import torch
+    return torch._C._cuda_getCurrentRawStream(_cache_shapes[handle][3]) or None
+
+
 def bs_cache_append(handle: int, step: CacheStep, k, v, stream=None) -> None:
     """Quantises k and v [n_tokens, heads, dim] (any token and head strides) into the
     pages of the step's positions."""
@@ -406,7 +414,7 @@ def bs_cache_append(handle: int, step: CacheStep, k, v, stream=None) -> None:
         raise ValueError("k and v must have one dtype")
     kp, kt, kh = _rows(k, "k", handle, step)
     vp, vt, vh = _rows(v, "v", handle, step)
-    st = lib.bs_cache_append(handle, step.ref, kp, kt, kh, vp, vt, vh, _dtype_code(k), _stream(stream))
+    st = lib.bs_cache_append(handle, step.ref, kp, kt, kh, vp, vt, vh, _dtype_code(k), _cache_stream(handle, stream))
     _check(st, "bs_cache_append")
 
 
@@ -420,7 +428,8 @@ def bs_cache_read(handle: int, step: CacheStep, k_out, v_out, stream=None) -> No
             ptr[i] = _rows(t, "k_out, v_out", handle, step)[0]
             if not t.is_contiguous() or t.dtype != first.dtype:
                 raise ValueError("k_out and v_out must be contiguous and of one dtype")
-    st = lib.bs_cache_read(handle, step.ref, ptr[0], ptr[1], 0 if first is None else _dtype_code(first), _stream(stream))
+    st = lib.bs_cache_read(handle, step.ref, ptr[0], ptr[1], 0 if first is None else _dtype_code(first),
+                           _stream(stream) if first is None else _cache_stream(handle, stream))
     _check(st, "bs_cache_read")
 
 
@@ -433,19 +442,21 @@ def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: f
     """out = attention of q [n_tokens, q_heads, dim] over the stored positions each row
     sees; ``scale`` defaults to dim ** -0.5, ``window`` 0 is unlimited, ``lse``
     [n_tokens, q_heads] fp32 or None."""
-    import torch
     ptr, tok, head = _rows(q, "q", handle, step, True)
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous() or out.device != q.device:
+    rows, q_heads, dim = shape = q.shape
+    device = q.device
+    if out.shape != shape or out.dtype is not q.dtype or not out.is_contiguous() or out.device != device:
         raise ValueError("out must be contiguous, with q's shape, dtype and device")
-    if lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous() or
-                            lse.device != q.device):
+    code = _dtype_code(q)
+    if lse is not None and (lse.shape != (rows, q_heads) or _dtype_codes.get(lse.dtype) != BS_F32 or not lse.is_contiguous() or
+                            lse.device != device):
         raise ValueError("lse must be contiguous fp32 [n_tokens, q_heads] on q's device")
-    if workspace is not None and workspace.device != q.device:
+    if workspace is not None and workspace.device != device:
         raise ValueError("the workspace must be on q's device")
-    st = lib.bs_cache_attention(handle, step.ref, ptr, tok, head, q.shape[1], _dtype_code(q),
-                                q.shape[2] ** -0.5 if scale is None else scale, window, out.data_ptr(), _ptr(lse),
-                                _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                _stream(stream))
+    st = lib.bs_cache_attention(handle, step.ref, ptr, tok, head, q_heads, code, dim ** -0.5 if scale is None else scale,
+                                window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                None if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.nbytes, _cache_stream(handle, stream))
     _check(st, "bs_cache_attention")
 
 
