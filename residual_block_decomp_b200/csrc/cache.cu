@@ -40,15 +40,17 @@ __device__ __forceinline__ int token_row(bool value, int t) { return value ? (t 
 
 template <typename T>
 struct Eight;   // 8 dense numbers
-// Whether some 16-bit number of two packed ones, signs aside, is at or above `least`.
-__device__ __forceinline__ bool reaches(uint4 a, uint32_t least) {
-  const uint32_t m = __vmaxu2(__vmaxu2(a.x & 0x7fff7fffu, a.y & 0x7fff7fffu), __vmaxu2(a.z & 0x7fff7fffu, a.w & 0x7fff7fffu));
-  return (m & 0xffffu) >= least || (m >> 16) >= least;
-}
 template <>
 struct Eight<__half> {
   uint4 a;
-  __device__ bool beyond() const { return reaches(a, 0x7bf0u); }   // the first fp16 number above 65000, inf, NaN
+  // Smallest and largest, NaN if there is one.
+  __device__ void range(float& lo, float& hi) const {
+    const __half2* h = reinterpret_cast<const __half2*>(&a);
+    const __half2 n = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
+    const __half2 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    lo = __half2float(__hmin_nan(__low2half(n), __high2half(n)));
+    hi = __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+  }
   __device__ void load(const void* p) { a = *static_cast<const uint4*>(p); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
@@ -72,7 +74,13 @@ struct Eight<__half> {
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 a;
-  __device__ bool beyond() const { return reaches(a, 0x477eu); }   // the first bf16 number above 65000, inf, NaN
+  __device__ void range(float& lo, float& hi) const {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&a);
+    const __nv_bfloat162 n = __hmin2_nan(__hmin2_nan(h[0], h[1]), __hmin2_nan(h[2], h[3]));
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3]));
+    lo = __bfloat162float(__hmin_nan(__low2bfloat16(n), __high2bfloat16(n)));
+    hi = __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+  }
   __device__ void load(const void* p) { a = *static_cast<const uint4*>(p); }
   __device__ void get(float (&x)[8]) const {
     const uint32_t r[4] = {a.x, a.y, a.z, a.w};
@@ -95,11 +103,11 @@ struct Eight<__nv_bfloat16> {
 template <>
 struct Eight<float> {
   float4 a, b;
-  __device__ bool beyond() const {
-    const float m = fmaxf(fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(a.z), fabsf(a.w))),
-                          fmaxf(fmaxf(fabsf(b.x), fabsf(b.y)), fmaxf(fabsf(b.z), fabsf(b.w))));
-    const float sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));   // NaN if one is
-    return m > kCacheClamp || sum != sum;
+  __device__ void range(float& lo, float& hi) const {
+    lo = fminf(fminf(fminf(a.x, a.y), fminf(a.z, a.w)), fminf(fminf(b.x, b.y), fminf(b.z, b.w)));
+    hi = fmaxf(fmaxf(fmaxf(a.x, a.y), fmaxf(a.z, a.w)), fmaxf(fmaxf(b.x, b.y), fmaxf(b.z, b.w)));
+    const float sum = ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w));   // NaN if one is, or of infinities
+    if (sum != sum) hi = sum;
   }
   __device__ void load(const void* p) {
     a = *static_cast<const float4*>(p);
@@ -153,12 +161,14 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       const int u = e * 32 + lane, hd = u / (2 * LR), kv = u / LR % 2, word = u % LR;
       float x[8];
       in[e].get(x);
-      if (in[e].beyond()) {
+      float lo, hi;
+      in[e].range(lo, hi);
+      if (!(lo >= -kCacheClamp && hi <= kCacheClamp)) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = x[k] != x[k] ? 0.0f : fminf(fmaxf(x[k], -kCacheClamp), kCacheClamp);
+        lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+        hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       }
-      float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-      float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
       for (int o = 1; o < 4; o *= 2) {           // a group is four lanes
         lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -167,20 +177,24 @@ __global__ void __launch_bounds__(kThreads) cache_append_kernel(const __grid_con
       const float step = __fdiv_rn(hi - lo, 15.0f);
       const __half sh = __float2half_rn(step), bh = __float2half_rn(fmaf(8.0f, step, lo));
       const float sf = __half2float(sh), bf = __half2float(bh);
-      // c = rint((x - b) / s + 8), by the reciprocal where that decides it: the quotient is at most 24 in size
-      // (8 + the rounding of s and b, or clamped beyond), so y is within 2^-16 of it, and so is the sum
-      const float inv = __frcp_rn(sf);
+      // c = rint((x - b) / s + 8) of the definition, by the reciprocal where that decides it: t = ((x - b) / s + 8) / 15
+      // clamped to [0, 1] is within 2^-22.5 of its value (the quotient's 2 ulp, the fma's half), and 15 t, like
+      // the definition's own sum, within 2^-18.  Codes are put together as fp32 integers below 2^16.
+      const float inv = __fdividef(1.0f, 15.0f * sf);
       constexpr float kInt = 12582912.0f;        // 1.5 2^23: adding it rounds to an integer
-      uint32_t w = 0;
-      float far[8], most = 0.0f;
+      float far[8], code[8], most = 0.0f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
-        const float y = fminf(fmaxf(fmaf(x[k] - bf, inv, 8.0f), 0.0f), 15.0f);
-        const float r = y + kInt;
-        far[k] = fabsf(y - (r - kInt));
+        const float t = __saturatef(fmaf(x[k] - bf, inv, 8.0f / 15.0f));
+        code[k] = fmaf(t, 15.0f, kInt) - kInt;
+        far[k] = fabsf(fmaf(t, 15.0f, -code[k]));
         most = fmaxf(most, far[k]);
-        w |= (__float_as_uint(r) & 15u) << (4 * k);
       }
+      uint32_t half[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        half[k] = __float_as_uint(fmaf(fmaf(fmaf(code[4 * k + 3], 16.0f, code[4 * k + 2]), 16.0f, code[4 * k + 1]), 16.0f, code[4 * k]) + 8388608.0f);
+      uint32_t w = __byte_perm(half[0], half[1], 0x5410);
       constexpr float kBorder = 0.5f - 0x1p-16f;
       if (!(sf > 0.0f)) {
         w = 0x88888888u;
