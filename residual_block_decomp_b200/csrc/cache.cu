@@ -7,12 +7,12 @@
 //
 // A group is s = fp16((max - min) / 15), b = fp16(min + 8 (max - min) / 15),
 // c = rint((x - b) / s + 8) in fp32.  A true division for every number made the writing kernel
-// compute bound (25 instructions a number); the reciprocal decides all codes but those
+// slower still; the reciprocal decides all codes but those
 // next to a rounding border, which are divided, so the codes are the definition's for every input.
 //
 // Bytes a (token, head): 4 D dense and 1.25 D packed.  Measured (8 heads of 128, bf16): writing prompts of 8417
-// tokens in all and reading them back 31 us together, 0.45 of the copy rate (writing takes 20 of them, bound by its
-// instructions, about 10 a number); reading contexts of 88 thousand tokens 163 us, 0.89 of it; one token written and
+// tokens in all and reading them back 28 us together, 0.49 of the copy rate (writing takes 18 of them, bound by its
+// instructions, 28 a number: half for the codes, the rest for ranges, pairs and addresses); reading contexts of 88 thousand tokens 163 us, 0.89 of it; one token written and
 // read back 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

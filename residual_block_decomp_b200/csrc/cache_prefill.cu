@@ -27,9 +27,11 @@
 // Q in shared memory, 64-token products 141 us, 128-token products 128 us: an operand in shared memory is read at 128
 // bytes a clock, and Q and K together take the products' whole time (or more, at 64 tokens) for it.  Q in tensor memory
 // halves that, and leaves room for two buffers of S with one group: 111 us; rows held by four neighbouring lanes instead
-// of two warps that meet 101; parts of split items joined by 16 warps 96.  What bounds it now: about 232 KB through
-// shared memory a tile of 128 x 128 (expanded keys 64, values 32, written once and read once, packed bytes 20 twice),
-// 1.8 thousand of its 2.9 thousand cycles, with the expansion's and the softmax's instructions beside it.
+// of two warps that meet 101; parts of split items joined by 16 warps 97.  What bounds it now: a tile of 128 x 128 takes
+// 2.9 thousand cycles, of which the expanding warps need 2.6, the rows' warps 2.6 and the products 2.0, each waiting for the
+// others a little; about 232 KB go through shared memory (expanded keys 64, values 32, written once and read once,
+// packed bytes 20 twice), 1.8 thousand cycles' worth.  Pairs of SMs (cta_group::2) that expand half a tile each
+// for 256 rows took 97 to 102 us: the products and the rows' warps then bound a tile.
 //
 // 8 numbers of a word are kept in the order (0, 4, 1, 5, 2, 6, 3, 7) that unpacking gives, in Q and K alike (a sum
 // does not mind), and in V as the order of O's columns, undone where rows are written.
