@@ -203,10 +203,16 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
 
 bs_status bs_cache_get_device_error(bs_cache_t cache) {
   if (cache == nullptr) return BS_ERR_INVALID_ARG;
+  // the whole device: the calls may have run on streams that a copy does not wait for
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess || (dev != cache->device && cudaSetDevice(cache->device) != cudaSuccess))
+    return BS_ERR_CUDA;
   uint32_t v = 0;
-  if (cudaMemcpy(&v, cache->err, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return BS_ERR_CUDA;
+  bool ok = cudaDeviceSynchronize() == cudaSuccess && cudaMemcpy(&v, cache->err, sizeof(v), cudaMemcpyDeviceToHost) == cudaSuccess;
+  if (ok && v != 0) ok = cudaMemset(cache->err, 0, sizeof(v)) == cudaSuccess && cudaDeviceSynchronize() == cudaSuccess;
+  if (dev != cache->device) cudaSetDevice(dev);
+  if (!ok) return BS_ERR_CUDA;
   if (v == 0) return BS_OK;
-  if (cudaMemset(cache->err, 0, sizeof(v)) != cudaSuccess) return BS_ERR_CUDA;
   return (v & kErrTimeout) ? BS_ERR_TIMEOUT : (v & kErrRange) ? BS_ERR_RANGE : BS_ERR_CUDA;
 }
 

@@ -654,6 +654,70 @@ def test_positions_up_to_the_largest(new):
     c.close()
 
 
+@pytest.mark.parametrize("new", [1, 40])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_slices_of_a_joined_projection_and_broadcast_heads(new, dim):
+    """q, k and v as slices of one tensor, heads before tokens, one row for all: as their contiguous copies."""
+    c = Case([(30, new), (5, new)], heads=2, dim=dim, page=16, seed=dim + new)
+    c.fill()
+    joined = c.numbers(c.rows, 8 + 2 + 2, torch.bfloat16)
+    q, k, v = joined[:, :8], joined[:, 8:10], joined[:, 10:]
+    want = c.attend(q.contiguous())
+    assert all(torch.equal(x, y) for x, y in zip(c.attend(q), want))
+    turned = q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert all(torch.equal(x, y) for x, y in zip(c.attend(turned), want))
+    got = torch.empty((4, c.rows, 2, dim), device="cuda")
+    R.bs_cache_append(c.handle, c.step, k, v)
+    R.bs_cache_read(c.handle, c.step, got[0], got[1])
+    R.bs_cache_append(c.handle, c.step, k.contiguous(), v.contiguous())
+    R.bs_cache_read(c.handle, c.step, got[2], got[3])
+    assert torch.equal(got[:2], got[2:])
+    one = joined[:1, 8:9].expand(c.rows, 2, dim)
+    R.bs_cache_append(c.handle, c.step, one, one)
+    R.bs_cache_read(c.handle, c.step, got[0], got[1])
+    assert (got[:2] == got[0, 0, 0]).all()
+    same = joined[:1, :1].expand(c.rows, 8, dim)
+    assert all(torch.equal(x, y) for x, y in zip(c.attend(same), c.attend(same.contiguous())))
+    c.close()
+
+
+def test_an_error_on_another_stream_is_read_without_waiting_for_it():
+    c = Case([(0, 3)], heads=1, dim=64, page=16, seed=51)
+    k = c.numbers(3, 1, torch.float16)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)             # some 10 ms
+        c.step.page_table.fill_(c.n_pages)
+        R.bs_cache_append(c.handle, c.step, k, k)
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_OK
+    c.close()
+
+
+def test_the_most_sequences_of_a_step():
+    gen = np.random.default_rng(52)
+    starts = gen.integers(0, 40, 4096)
+    c = Case([(int(s) if s % 9 else -1, 1) for s in starts], heads=1, dim=64, page=16, seed=52, cu=False)
+    c.fill(upto=[max(int(s), 0) + 1 for s in c.start])
+    q = c.numbers(4096, 2, torch.bfloat16)
+    out, lse = c.attend(q)
+    check_attention(c, q, out, lse)
+    assert R.bs_cache_get_device_error(c.handle) == R.BS_OK
+    c.close()
+
+
+@pytest.mark.parametrize("dim,n", [(64, 4096), (128, 400), (128, 2500), (256, 300)])
+def test_many_rows_of_many_sequences(dim, n):
+    """Row counts for the kernel for many rows, with as many sequences as its shared memory holds, and more."""
+    c = Case([(i % 50 if i % 31 == 0 else -1, 7) for i in range(n)], heads=1, dim=dim, page=16, seed=n, pages_more=0)
+    c.fill(upto=[int(s) + 7 if s >= 0 else 0 for s in c.start])
+    q = c.numbers(c.rows, 8, torch.bfloat16)
+    out, lse = c.attend(q)
+    check_attention(c, q, out, lse, sample=1)
+    c.close()
+
+
 def test_pages_beyond_four_gib():
     heads, dim, page = 8, 128, 64
     n_pages = (9 << 29) // R.bs_cache_page_bytes(heads, dim, page)
