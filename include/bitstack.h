@@ -458,8 +458,11 @@ size_t bs_cache_attention_workspace_bytes(bs_cache_t cache, const bs_cache_step*
  * -inf; a row of q with an infinity or a NaN gets NaN, and no other row does.
  * Scores, the softmax's maximum and sum and the accumulated output are fp32; the
  * dequantised values enter the product in fp16 (half a step), and so do the weights
- * exp(s - max) of BF16 rows (those of F16 rows in two fp16 parts).  Results do not
- * depend on timing: the same step gives the same bits.
+ * exp(s - max) of BF16 rows (those of F16 rows in two fp16 parts), in a range that ends
+ * 2^-32 below the row's largest: a weight smaller than that counts in lse and in the
+ * denominator only.  The values' rounding makes the error of an F16 result about 1.4
+ * times what its own rounding alone would.  Results do not depend on timing: the same
+ * step gives the same bits.
  * Few rows a head run on one kernel, many on another, whose waits are bounded
  * (500 ms); one that runs out is reported as BS_ERR_TIMEOUT, and the workspace has to
  * be zeroed again then.  BS_ERR_INVALID_ARG for a scale that is not finite (times

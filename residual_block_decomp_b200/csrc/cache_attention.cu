@@ -26,8 +26,11 @@
 //    A query row enters as fp16, scaled by a power of two to have its largest entry in [1, 2) (undone in
 //    the fp32 scores): exact down to 2^-14 of that entry (bf16: 2^-17), and within 2^-25 of it below.
 //  * Softmax: the accumulator layout holds rows = tokens, columns = query rows.  The reference m of the weights
-//    2^(x - m) follows the running maximum only when a score passes it by more than 8 (weights stay below 2^8,
-//    far inside fp16): most tiles then need no shuffles and no rescaling, only a vote.
+//    2^(x - m) is taken 7 below the running maximum, and again only when a score passes it by more than 15 (weights
+//    stay at or below 2^15, inside fp16): most tiles then need no shuffles and no rescaling, only a vote.  The 7
+//    puts fp16's smallest half step, 2^-25, at 2^-32 of the largest weight: with the reference at the maximum the
+//    weights of a long flat tail behind one large score, 2^-25 of it each, were all lost to the product, though not to
+//    the sum (0.3 % of the row for 128K of them).
 //    movmatrix turns the fp16 weights into the next product's B fragment.  Rows that are fp16 themselves take the
 //    weights in two fp16 parts: one rounding of the weights and that of the values together moved an fp16 result by
 //    1.5 times what its own rounding does, the values' alone move it by 1.3 to 1.4 times (4 sequences of 128K: 144 ->
@@ -58,7 +61,8 @@ constexpr int kTileBytes5k = 5120;
 constexpr int kWarps = 12;
 constexpr float kNegInf = -INFINITY;
 constexpr float kNothing = -3.0e38f;   // the reference before any score
-constexpr float kLag = 8.0f;           // how far scores may pass it
+constexpr float kHead = 7.0f;          // how far below the largest score it is taken
+constexpr float kLag = 15.0f;          // how far scores may pass it
 
 template <int D, int NT>
 struct Cfg {
@@ -500,7 +504,7 @@ struct State {
         for (int k = 0; k < 2; ++k) {
 #pragma unroll
           for (int o2 = 4; o2 < 32; o2 *= 2) mx[nt][k] = fmaxf(mx[nt][k], __shfl_xor_sync(0xffffffffu, mx[nt][k], o2));
-          const float mn = fmaxf(m[nt][k], mx[nt][k]);
+          const float mn = fmaxf(m[nt][k], mx[nt][k] - kHead);
           corr[k] = ex2(m[nt][k] - mn);
           m[nt][k] = mn;
           l[nt][k] *= corr[k];

@@ -8,8 +8,8 @@
 //     S = Q K^T             (Q and S in tensor memory, K in shared memory, fp32 sums)
 //     P = 2^(S f - m)       as fp16 (two parts for fp16 rows, as in the kernel for few), over S in tensor memory
 //     O += P V              (P and O in tensor memory, V in shared memory with the dims contiguous)
-// with the maximum and sum of a row in registers.  As in the kernel for few rows the reference m follows the maximum
-// only when a score passes it by 8 (weights up to 2^8), so O is hardly ever rescaled.
+// with the reference and sum of a row in registers.  As in the kernel for few rows the reference m lies 7 below the
+// maximum and follows it only when a score passes it by 15 (weights up to 2^15), so O is hardly ever rescaled.
 //
 // Scores stay exact to fp32: a key is b + s (c - 8); s (c - 8) / 2 has 15 bits, so fp16 parts hi = round(s (c - 8) / 2)
 // and lo = the fma's remainder hold it exactly (halved, as s (c - 8) alone may pass fp16's range), and the b of a group
@@ -47,7 +47,8 @@ namespace bs {
 namespace {
 
 constexpr float kNothing = -3.0e38f;    // the reference before any score
-constexpr float kLag = 8.0f;            // how far scores may pass it
+constexpr float kHead = 7.0f;           // how far below the largest score it is taken
+constexpr float kLag = 15.0f;           // how far scores may pass it
 
 // A run of tiles of one item: tiles t0 .. t1 - 1 of `tiles`.
 struct Segment {
@@ -554,7 +555,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           float keep[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float mn = top[k] > m[k] + kLag ? top[k] : m[k];
+            const float mn = top[k] > m[k] + kLag ? top[k] - kHead : m[k];
             keep[k] = ex2(m[k] - mn);
             l[k] *= keep[k];
             m[k] = mn;
@@ -573,6 +574,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
             }
           }
         }
+        // a tile's weights are summed by themselves: one by one, those below 2^-25 of a long context's sum would be lost
+        float sum[2] = {0.0f, 0.0f};
 #pragma unroll 1
         for (int c = 0; c < BT; c += 64) {
           load(c);
@@ -581,8 +584,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           for (int j = 0; j < 32; j += 4) {
             const float a = ex2(fmaf(__uint_as_float(x[j]), f[0], -m[0])), b = ex2(fmaf(__uint_as_float(x[j + 1]), f[0], -m[0]));
             const float d = ex2(fmaf(__uint_as_float(x[j + 2]), f[1], -m[1])), e = ex2(fmaf(__uint_as_float(x[j + 3]), f[1], -m[1]));
-            l[0] += a + b;
-            l[1] += d + e;
+            sum[0] += a + b;
+            sum[1] += d + e;
             pr[j / 2] = h2u(__floats2half2_rn(a, b));
             pr[j / 2 + 1] = h2u(__floats2half2_rn(d, e));
             x[j] = __float_as_uint(a);
@@ -600,6 +603,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
             tmem_st_pairs(s_at + c + 32, pr);
           }
         }
+        l[0] += sum[0];
+        l[1] += sum[1];
         tc_wait_st();
         tc_fence_before();
         __syncwarp();

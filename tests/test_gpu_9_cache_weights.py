@@ -1,0 +1,72 @@
+"""GPU: what the attention kernels of the packed cache make of small weights, of positions that nobody stored, and of
+very large scores: exact constructions, whose results are known in closed form."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import residual_block_decomp_b200 as R
+
+pytestmark = pytest.mark.gpu
+
+HALF = {torch.float16: 2.0 ** -11, torch.bfloat16: 2.0 ** -8}   # half a step, relative
+LOG2E = 1.4426950408889634
+
+
+def pool_of(keys, values, heads, page, spare=1):
+    """A pool that holds one sequence of constant rows: token t's numbers are keys[t] and values[t] (exact: a group of
+    equal numbers is its fp16 base).  (handle, the sequence's pages, the store)."""
+    dim, n = keys[1], len(keys[0])
+    n_pages = -(-n // page) + spare
+    store = torch.full((R.bs_cache_device_bytes(heads, dim, page, n_pages),), 0xff, dtype=torch.uint8, device="cuda")
+    handle = R.bs_cache_create(heads, dim, page, n_pages, store)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    k, v = (torch.as_tensor(x, dtype=torch.float16, device="cuda")[:, None, None].expand(n, heads, dim).contiguous()
+            for x in (keys[0], values))
+    R.bs_cache_append(handle, R.CacheStep(zero, table, n, n, cu), k, v)
+    return handle, table, store
+
+
+def attend(handle, step, q, scale, window=0):
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    ws = torch.zeros(R.bs_cache_attention_workspace_bytes(handle, step, q.shape[1]), dtype=torch.uint8, device="cuda")
+    R.bs_cache_attention(handle, step, q, out, ws, scale, window, lse)
+    torch.cuda.synchronize()
+    return out.double().cpu(), lse.double().cpu()
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [2, 64])                # the kernel for few rows, and the one for many
+def test_a_long_flat_tail_behind_one_large_score(group, dim, dtype):
+    """One key whose score is `gap` (in powers of two) above that of all others, as an attention sink is; its value is 0
+    and theirs are 1, so the result is the others' share.  A weight enters the product of the values in fp16 with the
+    largest at 2^7 or above: half of the smallest step, 2^-25, is 2^-32 of the largest weight, and a bf16 row's
+    weights are rounded once (2^-11).  A score is off by a few fp32 steps of itself.  The sum of the weights is off by half
+    a step, 2^-24 of it, an addition to the lane's share that holds the large one: n / 16 additions (few rows), n / 128."""
+    heads, n, seqs = 4, 20000, 64
+    keys = np.zeros(n)
+    keys[0] = 1.0
+    values = np.ones(n)
+    values[0] = 0.0
+    handle, table, _ = pool_of((keys, dim), values, heads, 64)
+    step = R.CacheStep(torch.full((seqs,), n - 1, dtype=torch.int32, device="cuda"), table.repeat(seqs, 1), seqs)
+    q = torch.ones(seqs, heads * group, dim, dtype=dtype, device="cuda")
+    for gap in (12.0, 23.7, 25.2, 27.6, 30.0):
+        out, lse = attend(handle, step, q, gap / (dim * LOG2E))
+        p = 2.0 ** -gap
+        z = 1 + (n - 1) * p
+        want = (n - 1) * p / z
+        part = (gap * 8 * 2.0 ** -23 + (n / 8) * 2.0 ** -23) * want + (n - 1) * 2.0 ** -32 * 1.01 / z
+        if dtype == torch.bfloat16:
+            part += 2.0 ** -11 * want
+        tol = part + HALF[dtype] * (want + part) + 2.0 ** -25
+        err = (out - want).abs().max().item()
+        assert err <= tol, (gap, want, err, tol)
+        want_lse = gap * math.log(2) + math.log(z)
+        assert (lse - want_lse).abs().max().item() <= 2.0 ** -20 * want_lse + n / (16 if group == 2 else 128) * 2.0 ** -24, gap
+    R.bs_cache_destroy(handle)
