@@ -1,0 +1,51 @@
+"""GPU: attention over the packed cache within the roundings that its kernels are allowed (tests/cache_check.py), few query
+rows a head and many, all head sizes, both types, with masks, peaked scores and long contexts."""
+import numpy as np
+import pytest
+import torch
+
+import residual_block_decomp_b200 as R
+from tests import cache_check as cc
+
+pytestmark = pytest.mark.gpu
+
+TYPES = {"fp16": torch.float16, "bf16": torch.bfloat16}
+
+
+def attend(made):
+    """(out, lse) in float64 of a cc.Made step, its pool's bytes on the GPU as the oracle made them."""
+    pool = made.pool
+    nbytes = R.bs_cache_device_bytes(pool.heads, pool.dim, pool.page_tokens, pool.n_pages)
+    store = torch.zeros(nbytes, dtype=torch.uint8, device="cuda")
+    store[:len(pool.data)] = torch.from_numpy(pool.data).cuda()
+    handle = R.bs_cache_create(pool.heads, pool.dim, pool.page_tokens, pool.n_pages, store)
+    start, table, cu = (torch.from_numpy(a).cuda() for a in (made.start, made.table, made.cu))
+    step = R.CacheStep(start, table, made.rows, made.max_new, cu)
+    q = torch.from_numpy(made.q).cuda().to(TYPES[made.dtype])
+    assert np.array_equal(q.float().cpu().numpy(), made.q)
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    ws = torch.zeros(R.bs_cache_attention_workspace_bytes(handle, step, q.shape[1]), dtype=torch.uint8, device="cuda")
+    R.bs_cache_attention(handle, step, q, out, ws, made.scale, made.window, lse)
+    assert R.bs_cache_get_device_error(handle) == R.BS_OK
+    R.bs_cache_destroy(handle)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("name", cc.CASES)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_within_the_roundings(name, dtype):
+    for seed in (0, 1):
+        made = cc.Made(**cc.CASES[name], dtype=dtype, seed=10 * len(name) + seed)
+        used = made.check(*attend(made))
+        print(f"{name} {dtype}: {used:.3f} of the tolerance")
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new,group", [(1, 4), (1, 9), (3, 20), (140, 2)])
+def test_long_and_many(dim, new, group):
+    """One context over all SMs, and sequences by the dozen."""
+    made = cc.Made([(9000, new)], heads=1, dim=dim, group=group, page=64, dtype="fp16", seed=new)
+    made.check(*attend(made), sample=4)
+    made = cc.Made([(7 * i - 1, new) for i in range(70)], heads=2, dim=dim, group=group, page=16, dtype="bf16", seed=dim)
+    made.check(*attend(made), sample=2)
