@@ -448,6 +448,7 @@ size_t bs_cache_attention_workspace_bytes(bs_cache_t cache, const bs_cache_step*
 
 /* out[r, h] = sum_t p_t v_t / sum_t p_t, p_t = exp(scale q[r, h] . k_t), over the stored
  * positions t that row r sees: 0 .. its own, the last `window` of them when window > 0.
+ * Positions that no row of a sequence sees need not be stored, nor their pages be there.
  * Query head h reads key/value head h / (q_heads / heads); q_heads is a multiple of the
  * cache's heads.  The step's own keys and values are read from the cache, so append
  * them first (on the same stream).

@@ -406,14 +406,16 @@ struct State {
         for (int o2 = 4; o2 < 32; o2 *= 2) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], o2);
   }
 
-  // One tile: positions pos0 .., of which `ok` chunks hold tokens; `masked`: some (row, token) is hidden.
-  // FINE: weights in two fp16 parts.
+  // One tile: positions pos0 .., of which `ok` chunks hold tokens; the sequence's rows see begin .. end - 1; `masked`: some
+  // (row, token) is hidden.  FINE: weights in two fp16 parts.
   template <bool FINE>
-  __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int end, uint32_t ok, bool masked, int window, int lane) {
+  __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int begin, int end, uint32_t ok, bool masked, int window, int lane) {
     const int t = lane >> 2, cc = lane & 3;
-    if (pos0 + C::TILE > end) {
-      // rows behind the context may hold anything: their values become 0 + 0 (c - 8), as 0 times them has to be 0
-      for (int i = end - pos0 + lane; i < C::TILE; i += 32) {
+    if (pos0 + C::TILE > end || pos0 < begin) {
+      // tokens behind the context, or in its first chunk before the window, may hold anything: their values become
+      // 0 + 0 (c - 8), as 0 times them has to be 0
+      for (int i = lane; i < C::TILE; i += 32) {
+        if (pos0 + i >= begin && pos0 + i < end) continue;
         uint32_t* pr = reinterpret_cast<uint32_t*>(st + (i >> 4) * chunk_bytes(D) + 18 * D + (((i & 15) >> 1) + 8 * (i & 1)) * (D / 8));
 #pragma unroll
         for (int g = 0; g < C::GR; ++g) pr[g] = 0;
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
       const int pos0 = c.first + c.t * C::TILE;
       const uint32_t ok = have & ((1u << C::TM) - 1);
       const bool masked = ok != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest || pos0 <= q.highest - p.window;
-      st.template tile<FINE>(q, sh.stage[warp][slot], pos0, c.end, ok, masked, p.window, lane);
+      st.template tile<FINE>(q, sh.stage[warp][slot], pos0, c.start - p.window + 1, c.end, ok, masked, p.window, lane);
       __syncwarp();
       ask(slot);
       slot = slot + 1 == C::ST ? 0 : slot + 1;

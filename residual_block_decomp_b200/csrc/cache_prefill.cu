@@ -96,7 +96,8 @@ struct alignas(1024) PShared {
   long long scan_total, wsum[32];
   uint32_t tmem;
   int abort, last[2];
-  int good[8], live[8];                     // of tile i % 8: the chunks that are in the pool, the tokens of the context
+  int good[8], from[8], live[8];            // of tile i % 8: the chunks that are in the pool, the tokens from .. live - 1
+                                            // that some row of the item sees
   // then long long prefix[n_seqs + 1]
 };
 
@@ -729,8 +730,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         ok = wait(&sh.cfull[1][j & 1], j >> 1) && (j < C::VST || wait(&sh.vempty[vs], j / C::VST - 1));
         if (!ok) break;
         const uint8_t* tb = sh.staging[1][j & 1];
-        const int good = sh.good[j & 7], live = sh.live[j & 7];
-        // V: rows of tokens as they are; tokens behind the item's context become zeros
+        const int good = sh.good[j & 7], from = sh.from[j & 7], live = sh.live[j & 7];
+        // V: rows of tokens as they are; tokens behind the item's context, and in its first chunk before the window, become
+        // zeros: they may hold anything
 #pragma unroll
         for (int k = 0; k < BT * (D / 32) / C::XT; ++k) {
           constexpr int UR = D / 32;
@@ -741,7 +743,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           const uint4 cw = *reinterpret_cast<const uint4*>(ch + (pr & 15) * (D / 2) + c * 16);
           const uint32_t w4[4] = {cw.x, cw.y, cw.z, cw.w};
           const uint32_t* prs = reinterpret_cast<const uint32_t*>(ch + 8 * D + (pr & 15) * (D / 8));
-          const bool there = row < live && ((good >> (row >> 4)) & 1);
+          const bool there = row >= from && row < live && ((good >> (row >> 4)) & 1);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int place = 4 * c + e, w = place / C::H + 8 * (place % C::H);       // C::H = D / 64
@@ -793,6 +795,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         const unsigned there = __ballot_sync(0xffffffffu, src != nullptr);
         if (lane == 0) {
           sh.good[i & 7] = static_cast<int>(there);
+          sh.from[i & 7] = max(sg.start + sg.rt * C::R / p.group - p.window + 1, 0) - pos0;
           sh.live[i & 7] = sg.end - pos0;
         }
 #pragma unroll

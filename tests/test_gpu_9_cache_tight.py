@@ -49,3 +49,15 @@ def test_long_and_many(dim, new, group):
     made.check(*attend(made), sample=4)
     made = cc.Made([(7 * i - 1, new) for i in range(70)], heads=2, dim=dim, group=group, page=16, dtype="bf16", seed=dim)
     made.check(*attend(made), sample=2)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 5, 70])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_only_the_windows_tokens_are_stored(dim, new, dtype):
+    """Positions that the window hides from every row hold NaN scales, also those in the same chunk as the first that is
+    seen: few rows and many, contexts whose windows begin at each place of a chunk."""
+    window = 20
+    seqs = [(100 + i, new) for i in range(16)] + [(19, new), (20, new), (5, new), (16 * 40 + 3, new)]
+    made = cc.Made(seqs, dim=dim, page=16, window=window, dtype=dtype, seed=dim + new, stored=[max(0, s - window + 1) for s, _ in seqs])
+    made.check(*attend(made))
