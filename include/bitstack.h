@@ -389,9 +389,12 @@ bs_status bs_plan_budget(long long n_steps, const int* order_weight, int n_weigh
  * position written twice by one call holds bytes of either row.
  * The arrays are checked on the device, before anything they point to is touched: a
  * sequence whose rows leave 0 .. n_tokens - 1, exceed max_new or run backwards, or
- * whose positions pass its row of the table or 2^31 - 512, is treated as an empty slot, and a page
- * outside the pool is not written, reads as zeros and is not attended; either sets
- * the pool's error word (bs_cache_get_device_error: BS_ERR_RANGE).
+ * whose positions pass its row of the table or 2^31 - 512, is treated as an empty slot
+ * (its rows are those of cu_new[i] .. cu_new[i + 1] - 1 that are inside 0 .. n_tokens -
+ * 1, none if they run backwards), and a page outside the pool is not written, reads as
+ * zeros and is not attended; either sets the pool's error word
+ * (bs_cache_get_device_error: BS_ERR_RANGE).  A row that two sequences name holds what
+ * either gives it, which may change from call to call.
  * Head sizes D: 64, 128, 256.  Page sizes: 16, 32, 64, 128 or 256 tokens. */
 typedef struct bs_cache_s* bs_cache_t; /* opaque handle of one layer's pool */
 

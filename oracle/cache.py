@@ -110,7 +110,9 @@ def spans(n_seqs, n_tokens, max_new, cu, start, table_width, page_tokens):
     for i in range(n_seqs):
         lo, hi = (int(cu[i]), int(cu[i + 1])) if cu is not None else (i, i + 1)
         bad = lo < 0 or hi < lo or hi > n_tokens
-        rows = 0 if bad else hi - lo
+        if bad:                       # the rows inside the dense tensors, as an empty slot's
+            lo, hi = max(lo, 0), min(hi, n_tokens)
+        rows = max(hi - lo, 0)
         live = not bad and start[i] >= 0 and rows > 0
         if live and (rows > max_new or int(start[i]) + rows > min(table_width * page_tokens, 2 ** 31 - 512)):
             live, bad = False, True

@@ -35,7 +35,8 @@ struct StepParams {
 };
 
 // What a step says of one sequence, after its checks: `rows` new tokens from row `row0`
-// at positions start ..; `live` false where nothing is stored or attended.
+// at positions start ..; `live` false where nothing is stored or attended.  Of rows that leave the dense tensors
+// those inside them remain.
 struct SeqSpan {
   int row0, rows, start;
   bool live, bad;
@@ -52,8 +53,13 @@ __device__ __forceinline__ SeqSpan seq_span(const StepParams& p, int i) {
   }
   const int start = p.start[i];
   s.bad = lo < 0 || hi < lo || hi > p.n_tokens;
+  if (s.bad) {
+    lo = lo < 0 ? 0 : lo;
+    hi = hi > p.n_tokens ? p.n_tokens : hi;
+    if (hi < lo) hi = lo;                        // none
+  }
   s.row0 = static_cast<int>(lo);
-  s.rows = s.bad ? 0 : static_cast<int>(hi - lo);
+  s.rows = static_cast<int>(hi - lo);
   s.start = start;
   s.live = !s.bad && start >= 0 && s.rows > 0;
   const long long end = static_cast<long long>(start) + s.rows;

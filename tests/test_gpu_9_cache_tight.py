@@ -6,6 +6,7 @@ import torch
 
 import residual_block_decomp_b200 as R
 from tests import cache_check as cc
+from tests.test_gpu_9_cache import Case
 
 pytestmark = pytest.mark.gpu
 
@@ -61,3 +62,47 @@ def test_only_the_windows_tokens_are_stored(dim, new, dtype):
     seqs = [(100 + i, new) for i in range(16)] + [(19, new), (20, new), (5, new), (16 * 40 + 3, new)]
     made = cc.Made(seqs, dim=dim, page=16, window=window, dtype=dtype, seed=dim + new, stored=[max(0, s - window + 1) for s, _ in seqs])
     made.check(*attend(made))
+
+
+@pytest.mark.parametrize("new", [2, 60])
+def test_rows_outside_the_tensors_are_an_empty_slots(new):
+    """A sequence whose rows begin before 0, end behind the last one, run backwards or lie far out: those inside the tensors
+    are attended and read as zeros, the others' results are as without it, nothing else is written."""
+    c = Case([(40, new), (50, new), (10, new)], heads=2, dim=64, page=16, seed=new, spare_rows=3)
+    c.fill()
+    q = c.numbers(c.rows, 8, torch.float16)
+    good, good_lse = c.attend(q)
+    cu = c.cu.copy()
+    for change, zero in [((0, -5), [(0, new)]), ((3, c.rows + 9), [(2 * new, c.rows)]), ((0, -2 ** 31), [(0, new)]),
+                         ((3, 2 ** 31 - 1), [(2 * new, c.rows)]), ((3, 2 * new - 1), []), ((0, new + 1), [])]:
+        c.cu = cu.copy()
+        c.cu[change[0]] = change[1]
+        step = c.make_step()
+        out, lse = c.attend(q, step=step)
+        assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE, change
+        k = torch.full((c.rows, 2, 64), 7.0, device="cuda")
+        v = k.clone()
+        R.bs_cache_read(c.handle, step, k, v)
+        assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE, change
+        bad = 0 if change[0] == 0 else 2                      # the sequence that is an empty slot
+        rest = torch.ones(c.rows, dtype=torch.bool, device="cuda")
+        rest[bad * new:(bad + 1) * new if bad == 0 else c.rows] = False
+        rest[3 * new:] = False
+        assert torch.equal(out[rest], good[rest]) and torch.equal(lse[rest], good_lse[rest]), change
+        assert (k[rest] != 7).any(2).all()
+        for a, b in zero:
+            assert (out[a:b] == 0).all() and (lse[a:b] == -np.inf).all() and (k[a:b] == 0).all() and (v[a:b] == 0).all(), change
+        if not zero:
+            rows = slice(bad * new, (bad + 1) * new)
+            assert (out[rows] == 7).all() and (lse[rows] == 7).all() and (k[rows] == 7).all(), change
+        before = c.store.clone()
+        R.bs_cache_append(c.handle, step, k, v)
+        torch.cuda.synchronize()
+        assert R.bs_cache_get_device_error(c.handle) == R.BS_ERR_RANGE, change
+        pages = torch.ones(c.n_pages, dtype=torch.bool, device="cuda")
+        pages[torch.from_numpy(np.unique(np.delete(c.table, bad, 0))).long().cuda()] = False
+        size = R.bs_cache_page_bytes(2, 64, 16)
+        now, was = (x[:c.n_pages * size].view(c.n_pages, size) for x in (c.store, before))
+        assert torch.equal(now[pages], was[pages]), change    # the empty slot's pages are as they were
+        c.store.copy_(before)
+    c.close()
