@@ -350,6 +350,7 @@ def bs_cache_destroy(handle: int) -> None:
     _cache_shapes.pop(handle, None)
 
 
+CACHE_MAX_SEQS = 4096   # sequences of a step
 _NO_CACHE = (None, None, None, None)
 _cache_shapes: dict[int, tuple] = {}   # (heads, dim, device, its index) of live handles, for the tensors' checks
 

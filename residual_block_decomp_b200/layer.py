@@ -195,6 +195,13 @@ class PageTable:
             self.length[s] += n
         return start, [self.pages[s] for s in seqs]
 
+    def undo(self, seqs, start, held) -> None:
+        """Takes the last advance of seqs back: their lengths, and the counts of pages they held."""
+        for s, a, n in reversed(list(zip(seqs, start, held))):
+            self.length[s] = a
+            self.free.extend(reversed(self.pages[s][n:]))
+            del self.pages[s][n:]
+
 
 class BitStackCache:
     """The packed key/value cache of a model: one pool of 4-bit pages a layer, and the
@@ -243,22 +250,30 @@ class BitStackCache:
         pages they need, and those of `room` more tokens a sequence, and moves the lengths
         on; rows of the dense tensors are the sequences' tokens end to end.  A captured
         step is taken further by copying a later step's ``start`` into its own, as far as
-        its room goes."""
-        seqs, new = list(seqs), [int(x) for x in new]
-        start, pages = self.table.advance(seqs, new, room)
-        width = max(1, max(map(len, pages)))
-        n = len(start)
-        if sum(new) > 2 ** 31 - 1:
+        its room goes.  Raises with nothing changed: for more than 4096 sequences, during a
+        capture (the step's arrays are copied from the host), or as PageTable.advance."""
+        seqs, new = [int(s) for s in seqs], [int(x) for x in new]
+        if len(seqs) > B.CACHE_MAX_SEQS or sum(new) > 2 ** 31 - 1:
             raise B.BsError(B.BS_ERR_RANGE, "BitStackCache.step")
-        host = np.zeros(2 * n + 1 + n * width, dtype=np.int32)
-        host[:n] = start
-        host[n + 1:2 * n + 1] = np.cumsum(np.asarray(new, dtype=np.int64))
-        rows = host[2 * n + 1:].reshape(n, width)
-        for r, p in zip(rows, pages):
-            r[:len(p)] = p
-        dev = torch.from_numpy(host).pin_memory().to(self.device, non_blocking=True)
-        cu = None if all(x == 1 for x in new) else dev[n:2 * n + 1]
-        return B.CacheStep(dev[:n], dev[2 * n + 1:].view(n, width), sum(new), max(new), cu)
+        if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("a step cannot be made during a capture: make it before, and copy later ones' start into it")
+        held = [len(self.table.pages.get(s, ())) for s in seqs]
+        start, pages = self.table.advance(seqs, new, room)
+        try:
+            width = max(1, max(map(len, pages)))
+            n = len(start)
+            host = np.zeros(2 * n + 1 + n * width, dtype=np.int32)
+            host[:n] = start
+            host[n + 1:2 * n + 1] = np.cumsum(np.asarray(new, dtype=np.int64))
+            rows = host[2 * n + 1:].reshape(n, width)
+            for r, p in zip(rows, pages):
+                r[:len(p)] = p
+            dev = torch.from_numpy(host).pin_memory().to(self.device, non_blocking=True)
+            cu = None if all(x == 1 for x in new) else dev[n:2 * n + 1]
+            return B.CacheStep(dev[:n], dev[2 * n + 1:].view(n, width), sum(new), max(new), cu)
+        except Exception:                             # no memory for its arrays
+            self.table.undo(seqs, start, held)
+            raise
 
     def append(self, step, k: torch.Tensor, v: torch.Tensor, layer: int = 0) -> None:
         """Packs k and v [rows, heads, dim] into the step's positions."""

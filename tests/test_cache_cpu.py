@@ -261,3 +261,52 @@ def test_page_table_refusals_change_nothing():
     t.advance([a, b], [31, 64])
     with pytest.raises(KeyError):
         t.close(17)
+
+
+def _cache_of(table):
+    """A BitStackCache without a pool: what step() does on the host."""
+    cache = R.BitStackCache.__new__(R.BitStackCache)
+    cache.table, cache.handles = table, []
+    cache.device = "cpu"
+    return cache
+
+
+def _state(t):
+    return dict(t.length), {k: list(v) for k, v in t.pages.items()}, list(t.free)
+
+
+def test_a_refused_step_changes_nothing(monkeypatch):
+    import torch
+    cache = _cache_of(R.PageTable(5000, 16))
+    seqs = [cache.open() for _ in range(4097)]
+    before = _state(cache.table)
+    with pytest.raises(R.BsError) as e:
+        cache.step(seqs, [1] * 4097)
+    assert e.value.status == R.BS_ERR_RANGE and _state(cache.table) == before
+    # rows that pass 32 bits together, though no sequence does
+    cache = _cache_of(R.PageTable(2 ** 23 + 8, 256))
+    seqs = [cache.open(), cache.open()]
+    with pytest.raises(R.BsError) as e:
+        cache.step(seqs, [2 ** 30, 2 ** 30 + 1])
+    assert e.value.status == R.BS_ERR_RANGE
+    assert cache.table.length == {0: 0, 1: 0} and len(cache.table.free) == 2 ** 23 + 8
+    # no memory for the step's arrays
+    cache = _cache_of(R.PageTable(20, 16))
+    seqs = [cache.open() for _ in range(3)]
+    cache.table.advance(seqs, [20, 1, 0])
+    before = _state(cache.table)
+
+    def none(self):
+        raise RuntimeError("out of memory")
+
+    monkeypatch.setattr(torch.Tensor, "pin_memory", none)
+    for new, room in (([40, 16, 1], 0), ([1, 1, 1], 30), ([0, 0, 0], 0)):
+        with pytest.raises(RuntimeError, match="out of memory"):
+            cache.step(seqs, new, room)
+        assert _state(cache.table) == before
+    # during a capture
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError, match="capture"):
+        cache.step(seqs, [1, 1, 1])
+    assert _state(cache.table) == before
