@@ -328,17 +328,22 @@ def bs_decompose(W, s, n_blocks: int, records, res_norms_sq, workspace, seed: in
 
 
 # ----------------------------------------------------------- packed key/value cache ---
+def _int(x: int) -> int:
+    """x as a C int; what none can hold becomes -1, which the library refuses (ctypes would cut it to 32 bits)."""
+    return x if -2 ** 31 <= x < 2 ** 31 else -1
+
+
 def bs_cache_page_bytes(heads: int, dim: int, page_tokens: int) -> int:
-    return int(lib.bs_cache_page_bytes(heads, dim, page_tokens))
+    return int(lib.bs_cache_page_bytes(_int(heads), _int(dim), _int(page_tokens)))
 
 
 def bs_cache_device_bytes(heads: int, dim: int, page_tokens: int, n_pages: int) -> int:
-    return int(lib.bs_cache_device_bytes(heads, dim, page_tokens, n_pages))
+    return int(lib.bs_cache_device_bytes(_int(heads), _int(dim), _int(page_tokens), _int(n_pages)))
 
 
 def bs_cache_create(heads: int, dim: int, page_tokens: int, n_pages: int, dev_pages, stream=None) -> int:
     h = ctypes.c_void_p()
-    st = lib.bs_cache_create(heads, dim, page_tokens, n_pages, _ptr(dev_pages),
+    st = lib.bs_cache_create(_int(heads), _int(dim), _int(page_tokens), _int(n_pages), _ptr(dev_pages),
                              dev_pages.numel() * dev_pages.element_size(), _stream(stream), ctypes.byref(h))
     _check(st, "bs_cache_create")
     _cache_shapes[h.value] = (heads, dim, dev_pages.device, dev_pages.get_device())
@@ -381,7 +386,8 @@ class CacheStep:
         self.device = start.device
         if page_table.device != start.device or (cu_new is not None and cu_new.device != start.device):
             raise ValueError("start, page_table and cu_new must be on one device")
-        self.c = _Step(n, self.n_tokens, self.max_new, page_table.shape[1], page_table.stride(0), pc, ps, pt)
+        self.c = _Step(_int(n), _int(self.n_tokens), _int(self.max_new), _int(page_table.shape[1]), _int(page_table.stride(0)),
+                       pc, ps, pt)
         self.ref = ctypes.byref(self.c)
 
 
@@ -435,7 +441,7 @@ def bs_cache_read(handle: int, step: CacheStep, k_out, v_out, stream=None) -> No
 
 
 def bs_cache_attention_workspace_bytes(handle: int, step: CacheStep, q_heads: int) -> int:
-    return int(lib.bs_cache_attention_workspace_bytes(handle, step.ref, q_heads))
+    return int(lib.bs_cache_attention_workspace_bytes(handle, step.ref, _int(q_heads)))
 
 
 def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: float | None = None, window: int = 0,
@@ -455,7 +461,7 @@ def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: f
     if workspace is not None and workspace.device != device:
         raise ValueError("the workspace must be on q's device")
     st = lib.bs_cache_attention(handle, step.ref, ptr, tok, head, q_heads, code, dim ** -0.5 if scale is None else scale,
-                                window, out.data_ptr(), None if lse is None else lse.data_ptr(),
+                                _int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
                                 None if workspace is None else workspace.data_ptr(),
                                 0 if workspace is None else workspace.nbytes, _cache_stream(handle, stream))
     _check(st, "bs_cache_attention")

@@ -310,3 +310,43 @@ def test_a_refused_step_changes_nothing(monkeypatch):
     with pytest.raises(RuntimeError, match="capture"):
         cache.step(seqs, [1, 1, 1])
     assert _state(cache.table) == before
+
+
+def test_numbers_that_no_c_int_holds_are_refused(monkeypatch):
+    """They would be cut to 32 bits: a window of 2^32 taken for none, 2^32 + 4 pages for 4."""
+    import torch
+    from residual_block_decomp_b200 import binding as B
+    big = 2 ** 32
+    assert R.bs_cache_device_bytes(8, 128, 64, big + 4) == 0 and R.bs_cache_device_bytes(big + 8, 128, 64, 4) == 0
+    assert R.bs_cache_page_bytes(8, big + 128, 64) == 0 and R.bs_cache_page_bytes(8, 128, big + 64) == 0
+    table, start = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    assert R.CacheStep(start, table, big + 1).c.n_tokens < 0
+    assert R.CacheStep(start, table, 1, big + 1).c.max_new < 0
+    seen, real = {}, B.lib
+
+    class Lib:
+        def __getattr__(self, name):
+            return getattr(real, name)
+
+        def bs_cache_attention(self, handle, step, q, tok, head, heads, dt, scale, window, *rest):
+            seen["window"] = window
+            return B.BS_OK
+
+        def bs_cache_create(self, *a):
+            seen["create"] = a[:4]
+            return B.BS_ERR_INVALID_ARG
+
+        def bs_cache_attention_workspace_bytes(self, handle, step, heads):
+            return max(0, heads)
+
+    monkeypatch.setattr(B, "lib", Lib())
+    monkeypatch.setattr(B, "_cache_stream", lambda *a: None)
+    monkeypatch.setitem(B._cache_shapes, 77, (1, 64, torch.device("cpu"), 0))
+    q = torch.zeros(1, 1, 64, dtype=torch.float16)
+    for window, given in ((0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, -1), (big, -1), (big + 7, -1), (-5, -5)):
+        R.bs_cache_attention(77, R.CacheStep(start, table, 1), q, torch.empty_like(q), None, window=window)
+        assert seen["window"] == given
+    with pytest.raises(R.BsError):
+        R.bs_cache_create(1, 64, 16, big + 1, torch.zeros(16))
+    assert seen["create"] == (1, 64, 16, -1)
+    assert R.bs_cache_attention_workspace_bytes(77, R.CacheStep(start, table, 1), big + 2) == 0
