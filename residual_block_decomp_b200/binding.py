@@ -342,6 +342,9 @@ def bs_cache_device_bytes(heads: int, dim: int, page_tokens: int, n_pages: int) 
 
 
 def bs_cache_create(heads: int, dim: int, page_tokens: int, n_pages: int, dev_pages, stream=None) -> int:
+    import torch
+    if not dev_pages.is_contiguous() or not dev_pages.is_cuda or dev_pages.get_device() != torch.cuda.current_device():
+        raise ValueError("the pool must be contiguous memory of the current GPU")
     h = ctypes.c_void_p()
     st = lib.bs_cache_create(_int(heads), _int(dim), _int(page_tokens), _int(n_pages), _ptr(dev_pages),
                              dev_pages.numel() * dev_pages.element_size(), _stream(stream), ctypes.byref(h))
@@ -458,8 +461,8 @@ def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: f
     if lse is not None and (lse.shape != (rows, q_heads) or _dtype_codes.get(lse.dtype) != BS_F32 or not lse.is_contiguous() or
                             lse.device != device):
         raise ValueError("lse must be contiguous fp32 [n_tokens, q_heads] on q's device")
-    if workspace is not None and workspace.device != device:
-        raise ValueError("the workspace must be on q's device")
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be contiguous, on q's device")
     st = lib.bs_cache_attention(handle, step.ref, ptr, tok, head, q_heads, code, dim ** -0.5 if scale is None else scale,
                                 _int(window), out.data_ptr(), None if lse is None else lse.data_ptr(),
                                 None if workspace is None else workspace.data_ptr(),

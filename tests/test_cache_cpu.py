@@ -346,7 +346,45 @@ def test_numbers_that_no_c_int_holds_are_refused(monkeypatch):
     for window, given in ((0, 0), (7, 7), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, -1), (big, -1), (big + 7, -1), (-5, -5)):
         R.bs_cache_attention(77, R.CacheStep(start, table, 1), q, torch.empty_like(q), None, window=window)
         assert seen["window"] == given
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    class Pool(torch.Tensor):                                # of GPU 0, as far as the binding sees
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
     with pytest.raises(R.BsError):
-        R.bs_cache_create(1, 64, 16, big + 1, torch.zeros(16))
+        R.bs_cache_create(1, 64, 16, big + 1, torch.zeros(16).as_subclass(Pool), stream=0)
     assert seen["create"] == (1, 64, 16, -1)
     assert R.bs_cache_attention_workspace_bytes(77, R.CacheStep(start, table, 1), big + 2) == 0
+
+
+def test_memory_that_is_not_what_it_looks_like_is_refused(monkeypatch):
+    """A pool in host memory, on another GPU, or of one byte seen a million times; a workspace of one byte."""
+    import torch
+    from residual_block_decomp_b200 import binding as B
+    real = B.lib
+
+    class Lib:
+        def __getattr__(self, name):
+            assert name == "bs_status_string", f"{name} was called"
+            return getattr(real, name)
+
+    class Pool(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    monkeypatch.setattr(B, "lib", Lib())
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for pool in (torch.zeros(1 << 20, dtype=torch.uint8), torch.zeros(1 << 20, dtype=torch.uint8).as_subclass(Pool),
+                 torch.zeros(1, dtype=torch.uint8).expand(1 << 20)):
+        with pytest.raises(ValueError, match="pool"):
+            R.bs_cache_create(1, 64, 16, 4, pool)
+    monkeypatch.setitem(B._cache_shapes, 77, (1, 64, torch.device("cpu"), 0))
+    table, start = torch.zeros(1, 3, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    q = torch.zeros(1, 1, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="workspace"):
+        R.bs_cache_attention(77, R.CacheStep(start, table, 1), q, torch.empty_like(q), torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
