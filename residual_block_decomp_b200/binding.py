@@ -354,8 +354,8 @@ def bs_cache_create(heads: int, dim: int, page_tokens: int, n_pages: int, dev_pa
 
 
 def bs_cache_destroy(handle: int) -> None:
+    _cache_shapes.pop(handle, None)   # first: once it is free, another thread's new handle may be the same number
     _check(lib.bs_cache_destroy(handle), "bs_cache_destroy")
-    _cache_shapes.pop(handle, None)
 
 
 CACHE_MAX_SEQS = 4096   # sequences of a step

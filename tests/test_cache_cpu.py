@@ -388,3 +388,17 @@ def test_memory_that_is_not_what_it_looks_like_is_refused(monkeypatch):
     q = torch.zeros(1, 1, 64, dtype=torch.float16)
     with pytest.raises(ValueError, match="workspace"):
         R.bs_cache_attention(77, R.CacheStep(start, table, 1), q, torch.empty_like(q), torch.zeros(1, dtype=torch.uint8).expand(1 << 24))
+
+
+def test_a_handle_that_is_made_again_while_it_is_destroyed_keeps_its_shape(monkeypatch):
+    from residual_block_decomp_b200 import binding as B
+
+    class Lib:
+        def bs_cache_destroy(self, handle):
+            B._cache_shapes[handle] = "another thread's"     # as its bs_cache_create does with the memory just freed
+            return B.BS_OK
+
+    monkeypatch.setattr(B, "lib", Lib())
+    monkeypatch.setitem(B._cache_shapes, 77, "mine")
+    R.bs_cache_destroy(77)
+    assert B._cache_shapes[77] == "another thread's"
