@@ -43,6 +43,7 @@ class BitStackLinear:
         self.host_records: list[torch.Tensor] = []   # the storage copy of every block, pinned
         self._inflight: list[torch.Tensor] = []
         self._ws: torch.Tensor | None = None
+        self._outgrown: list[torch.Tensor] = []   # captured graphs may still use them
 
     # ----------------------------------------------------------- storage side ----
     def add_record(self, record) -> int:
@@ -92,8 +93,13 @@ class BitStackLinear:
         if need == 0:
             return None
         if self._ws is None or self._ws.numel() < need:
+            ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            if torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing():
+                return ws   # the graph's own, which its replays zero: nothing has zeroed it for other calls
+            if self._ws is not None:
+                self._outgrown.append(self._ws)
             # zeroed once: completed calls leave it consistent (device_error re-zeroes it)
-            self._ws = torch.zeros(need, dtype=torch.uint8, device=self.device)
+            self._ws = ws
         return self._ws
 
     def forward(self, x: torch.Tensor, n_loaded: int | None = None, out: torch.Tensor | None = None,
@@ -126,10 +132,11 @@ class BitStackLinear:
 
     def device_error(self) -> int:
         """Reads and clears the stack's sticky device error word.  After an error the
-        workspace's counters may be stale, so the layer's own workspace is zeroed."""
+        workspace's counters may be stale, so the layer's own workspaces are zeroed."""
         status = B.bs_get_device_error(self.handle)
-        if status != B.BS_OK and self._ws is not None:
-            self._ws.zero_()
+        if status != B.BS_OK:
+            for ws in self._outgrown + ([] if self._ws is None else [self._ws]):
+                ws.zero_()
         return status
 
     def close(self) -> None:
