@@ -191,9 +191,15 @@ struct Worker {
       else hi = mid - 1;
     }
     seq(c, lo);
-    const unsigned off = static_cast<unsigned>(tile - prefix[lo]);
-    const unsigned item = off / c.tiles;
-    c.t = off % c.tiles;
+    const unsigned long long off = static_cast<unsigned long long>(tile - prefix[lo]);
+    unsigned item;                         // fewer than 2^31 of a sequence
+    if (off >> 32 == 0) {                  // (divisions in 32 bits where they can be)
+      item = static_cast<unsigned>(off) / c.tiles;
+      c.t = static_cast<unsigned>(off) % c.tiles;
+    } else {
+      item = static_cast<unsigned>(off / c.tiles);
+      c.t = static_cast<int>(off % c.tiles);
+    }
     c.h = item / c.rts;
     c.rt = item % c.rts;
   }
@@ -752,9 +758,9 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
                                   : (T + gridDim.x - 1) / gridDim.x,
                             static_cast<long long>(C::NW));
   const long long c0 = per * blockIdx.x, c1 = max(min(c0 + per, T), c0);
-  const uint32_t share = static_cast<uint32_t>(c1 - c0);
-  const long long w0 = c0 + static_cast<unsigned long long>(share) * warp / C::NW,
-                  w1 = c0 + static_cast<unsigned long long>(share) * (warp + 1) / C::NW;
+  const long long share = c1 - c0;
+  const long long w0 = c0 + (small ? static_cast<uint32_t>(share) * static_cast<uint32_t>(warp) / C::NW : share * warp / C::NW),
+                  w1 = c0 + (small ? static_cast<uint32_t>(share) * static_cast<uint32_t>(warp + 1) / C::NW : share * (warp + 1) / C::NW);
   // Rows that see nothing, and the step's errors: the last CTAs, which have the least to do.
   for (int i = gridDim.x - 1 - blockIdx.x; i < p.st.n_seqs; i += gridDim.x) {
     const SeqSpan s = seq_span(p.st, i);

@@ -70,3 +70,25 @@ def test_a_long_flat_tail_behind_one_large_score(group, dim, dtype):
         want_lse = gap * math.log(2) + math.log(z)
         assert (lse - want_lse).abs().max().item() <= 2.0 ** -20 * want_lse + n / (16 if group == 2 else 128) * 2.0 ** -24, gap
     R.bs_cache_destroy(handle)
+
+
+def test_more_tiles_of_a_sequence_than_32_bits_count():
+    """1024 heads of a context of 12.3 million tokens, 48 rows each: 4.7 10^9 tiles of 16 tokens.  Every page is the same
+    one; keys are zeros, so the weights are equal, and a head's values are 1 or 2: all sums are exact.  (About 5 seconds.)"""
+    heads, dim, group, page = 1024, 256, 48, 256
+    n = 12_300_032
+    assert n // 16 * heads * (group // 8) > 2 ** 32 + 2 ** 28 and n % page == 0
+    handle, _, _ = pool_of((np.zeros(page), dim), np.zeros(page), heads, page, spare=0)
+    level = 1.0 + torch.arange(heads, device="cuda") // 512
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    write = R.CacheStep(zero, zero[None], page, page, torch.tensor([0, page], dtype=torch.int32, device="cuda"))
+    R.bs_cache_append(handle, write, torch.zeros(page, heads, dim, dtype=torch.float16, device="cuda"),
+                      level.half()[None, :, None].expand(page, heads, dim).contiguous())
+    step = R.CacheStep(torch.full((1,), n - 1, dtype=torch.int32, device="cuda"), torch.zeros(1, n // page, dtype=torch.int32, device="cuda"), 1)
+    q = torch.randn(1, heads * group, dim, device="cuda").bfloat16()
+    out, lse = attend(handle, step, q, 0.0625)
+    assert R.bs_cache_get_device_error(handle) == R.BS_OK
+    want = level.double().cpu().repeat_interleave(group)[None, :, None]
+    assert torch.equal(out, want.expand_as(out))
+    assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -21 * math.log(n)
+    R.bs_cache_destroy(handle)
