@@ -502,7 +502,7 @@ struct State {
 #pragma unroll
         for (int mt = 1; mt < C::TM; ++mt) mx[nt][k] = fmaxf(mx[nt][k], fmaxf(s[mt][nt][k], s[mt][nt][2 + k]));
         mx[nt][k] *= q.factor[nt][k];
-        passed |= mx[nt][k] > m[nt][k] + kLag;
+        passed |= mx[nt][k] > __fadd_rd(m[nt][k], kLag);
       }
     if (__any_sync(0xffffffffu, passed)) {
 #pragma unroll
@@ -528,7 +528,13 @@ struct State {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][nt][e] = ex2(fmaf(s[mt][nt][e], q.factor[nt][e & 1], -m[nt][e & 1]));
+        for (int e = 0; e < 4; e += 2) {
+          // From rounded products, as m is one: with a fused one the difference is off by half a step of m, and scores
+          // from 2^26 on, whose steps are 8 and more, gave weights of 2^16 and more (infinities) or 0.
+          mul_sub2(s[mt][nt][e], s[mt][nt][e + 1], q.factor[nt][0], q.factor[nt][1], m[nt][0], m[nt][1]);
+          s[mt][nt][e] = ex2(s[mt][nt][e]);
+          s[mt][nt][e + 1] = ex2(s[mt][nt][e + 1]);
+        }
 #pragma unroll
     for (int mt = 0; mt < C::TM; ++mt) {
       uint32_t b[NT][2], lo[NT][2];

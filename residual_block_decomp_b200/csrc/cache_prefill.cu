@@ -552,11 +552,11 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
           top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2)) * f[k];
         }
-        if (__any_sync(0xffffffffu, top[0] > m[0] + kLag || top[1] > m[1] + kLag)) {
+        if (__any_sync(0xffffffffu, top[0] > __fadd_rd(m[0], kLag) || top[1] > __fadd_rd(m[1], kLag))) {
           float keep[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float mn = top[k] > m[k] + kLag ? top[k] - kHead : m[k];
+            const float mn = top[k] > __fadd_rd(m[k], kLag) ? top[k] - kHead : m[k];
             keep[k] = ex2(m[k] - mn);
             l[k] *= keep[k];
             m[k] = mn;
@@ -583,8 +583,11 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           uint32_t pr[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 4) {
-            const float a = ex2(fmaf(__uint_as_float(x[j]), f[0], -m[0])), b = ex2(fmaf(__uint_as_float(x[j + 1]), f[0], -m[0]));
-            const float d = ex2(fmaf(__uint_as_float(x[j + 2]), f[1], -m[1])), e = ex2(fmaf(__uint_as_float(x[j + 3]), f[1], -m[1]));
+            float a = __uint_as_float(x[j]), b = __uint_as_float(x[j + 1]);
+            float d = __uint_as_float(x[j + 2]), e = __uint_as_float(x[j + 3]);
+            mul_sub2(a, b, f[0], f[0], m[0], m[0]);             // rounded products, as the reference is one (see the kernel
+            mul_sub2(d, e, f[1], f[1], m[1], m[1]);             // for few rows)
+            a = ex2(a), b = ex2(b), d = ex2(d), e = ex2(e);
             sum[0] += a + b;
             sum[1] += d + e;
             pr[j / 2] = h2u(__floats2half2_rn(a, b));

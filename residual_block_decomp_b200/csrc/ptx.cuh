@@ -19,6 +19,18 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
+// ------------------------------------------------------------ packed fp32 ----------
+// a f - m for two numbers, product and difference rounded each: as many instructions as two fmas.  (The product as
+// a f + 0: a packed multiplication was put together with the subtraction.)
+__device__ __forceinline__ void mul_sub2(float& a0, float& a1, float f0, float f1, float m0, float m1) {
+  asm("{\n\t.reg .b64 a, f, m;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 f, {%2, %3};\n\tmov.b64 m, {%4, %5};\n\t"
+      "fma.rn.f32x2 a, a, f, %6;\n\tsub.rn.f32x2 a, a, m;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(a0), "+f"(a1)
+      : "f"(f0), "f"(f1), "f"(m0), "f"(m1), "l"(0ull));
+}
+
 // ------------------------------------------------- programmatic dependent launch --
 // A kernel launched with programmatic stream serialisation may start before the
 // kernel ahead of it in the stream has finished.  griddep_wait() blocks the calling

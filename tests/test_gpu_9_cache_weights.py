@@ -92,3 +92,50 @@ def test_more_tiles_of_a_sequence_than_32_bits_count():
     assert torch.equal(out, want.expand_as(out))
     assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -21 * math.log(n)
     R.bs_cache_destroy(handle)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group", [2, 64])                # the kernel for few rows, and the one for many
+def test_scores_of_any_size_that_fp32_holds(group, dim, dtype):
+    """Keys and queries of up to 10^4, and bf16 queries of 10^9 and 10^20: scores of 10^8 to 10^25, whose fp32 steps are far
+    larger than 1.  The largest score's value is the result wherever it is clear which that is.  A score is a sum of terms
+    s (64 + c) q and (72 s - b) sum q, 79 s at most for each q, where 15 s is a group's range, so 10.6 times its largest
+    number, with some 40 steps of 2^-23 of it in all: off by up to 2^-14 of sum |q| max |k|."""
+    heads, n, page = 2, 60, 16
+    gen = np.random.default_rng(dim + group)
+    n_pages = n // page + 1
+    store = torch.full((R.bs_cache_device_bytes(heads, dim, page, n_pages),), 0xff, dtype=torch.uint8, device="cuda")
+    handle = R.bs_cache_create(heads, dim, page, n_pages, store)
+    table = torch.arange(n_pages, dtype=torch.int32, device="cuda")[None]
+    zero, cu = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    write = R.CacheStep(zero, table, n, n, cu)
+    k, v = (torch.from_numpy(gen.standard_normal((n, heads, dim)).astype(np.float32) * s).cuda() for s in (5e3, 1.0))
+    R.bs_cache_append(handle, write, k, v)
+    R.bs_cache_read(handle, write, k, v)
+    k, v = k.double().cpu(), v.double().cpu()
+    for size in (1e4, 1.0) if dtype == torch.float16 else (1e4, 1e9, 1e20, 1.0):
+        for sign in (1, -1):
+            seqs = 40                                       # contexts of 1 to n tokens
+            start = torch.arange(seqs, dtype=torch.int32) * (n - 1) // (seqs - 1)
+            step = R.CacheStep(start.cuda(), table.repeat(seqs, 1), seqs)
+            q = (torch.from_numpy(gen.standard_normal((seqs, heads * group, dim)).astype(np.float32)) * size).to(dtype)
+            if sign < 0:                                    # every score far below zero
+                q = q.abs() * -k.mean((0, 1)).sign().to(dtype)
+            out, lse = attend(handle, step, q.cuda(), 1.0)
+            clear = 0
+            for i in range(seqs):
+                x = torch.einsum("hgd,thd->hgt", q[i].double().view(heads, group, dim), k[:int(start[i]) + 1]).flatten(0, 1)
+                top, at = x.max(-1)
+                rest = x.clone()
+                rest.scatter_(1, at[:, None], -math.inf)
+                off = 2.0 ** -14 * q[i].double().abs().sum(-1) * k.abs().max()
+                sure = top - rest.amax(-1) > 2 * off + 40
+                want = v[at, torch.arange(heads).repeat_interleave(group)]
+                err = (out[i] - want).abs()[sure] / (want.abs()[sure] * (HALF[dtype] + 2.0 ** -10) + 2.0 ** -25)
+                assert err.numel() == 0 or err.max().item() <= 1, (size, sign, i)
+                assert ((lse[i] - top).abs() <= off + 2.0 ** -21 * top.abs())[sure].all(), (size, sign, i)
+                assert torch.isfinite(out[i]).all() and torch.isfinite(lse[i]).all()
+                clear += int(sure.sum())
+            assert clear > 0.9 * seqs * heads * group
+    R.bs_cache_destroy(handle)
