@@ -75,6 +75,10 @@ struct Cfg {
   static constexpr int FREG = OREG + 4 * NT;                  // and its maxima and sums
   static constexpr int NW = (NT == 1 && D <= 128) ? kWarps : 8;   // warps
   static constexpr int ST = 2;                                // stages of a warp
+  // Tiles (4096 tokens) after which a warp's output is added to a sum in shared memory and begins anew.  A product cuts its
+  // terms off at the accumulator's last place instead of rounding them, so that sums of many tokens come out too
+  // small, by 2^-30 to 2^-28 of them a token: 0.05 % for a run of 128K, 0.4 % for 1M (an fp16 result's half step is 0.05 %).
+  static constexpr int FOLD = 4096 / TILE;
 };
 
 // Partial results are laid out [register][lane].
@@ -153,6 +157,7 @@ template <int D, int NT>
 struct Shared {
   using C = Cfg<D, NT>;
   uint8_t stage[C::NW][C::ST][kTileBytes5k];
+  float4 sum[C::NW][C::OREG / 4][32];   // State::fold of the lanes
   FragMeta meta[2 * C::NW];
   long long wsum[32];
   int last[2];            // slot of a shared item whose parts this CTA adds up; -1: none
@@ -391,6 +396,7 @@ struct State {
   using C = Cfg<D, NT>;
   float o[NT][C::J][4][4];
   float m[NT][2], l[NT][2];   // m: the weights' reference; l: this lane's tokens only until reduce()
+  bool folded;                // part of the output is in `sum`, with the same reference
 
   __device__ void clear() {
 #pragma unroll
@@ -402,6 +408,23 @@ struct State {
       m[nt][0] = m[nt][1] = kNothing;
       l[nt][0] = l[nt][1] = 0.0f;
     }
+    folded = false;
+  }
+  // The output so far goes to the sum (END: the sum comes back to the output).
+  template <bool END>
+  __device__ void fold(float4 (*sum)[32], int lane) {
+#pragma unroll
+    for (int i = 0; i < C::OREG / 4; ++i) {
+      float(&x)[4] = o[i / (4 * C::J)][i / 4 % C::J][i % 4];
+      const float4 s = END || folded ? sum[i][lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (END) {
+        x[0] += s.x; x[1] += s.y; x[2] += s.z; x[3] += s.w;
+      } else {
+        sum[i][lane] = make_float4(x[0] + s.x, x[1] + s.y, x[2] + s.z, x[3] + s.w);
+        x[0] = x[1] = x[2] = x[3] = 0.0f;
+      }
+    }
+    folded = !END;
   }
   __device__ void reduce() {
 #pragma unroll
@@ -415,7 +438,8 @@ struct State {
   // One tile: positions pos0 .., of which `ok` chunks hold tokens; the sequence's rows see begin .. end - 1; `masked`: some
   // (row, token) is hidden.  FINE: weights in two fp16 parts.
   template <bool FINE>
-  __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int begin, int end, uint32_t ok, bool masked, int window, int lane) {
+  __device__ void tile(const Rows<D, NT>& q, uint8_t* st, int pos0, int begin, int end, uint32_t ok, bool masked, int window,
+                       float4 (*sum)[32], int lane) {
     const int t = lane >> 2, cc = lane & 3;
     if (pos0 + C::TILE > end || pos0 < begin) {
       // tokens behind the context, or in its first chunk before the window, may hold anything: their values become
@@ -521,6 +545,12 @@ struct State {
         for (int j = 0; j < C::J; ++j)
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[nt][j][e / 4][e % 4] *= corr[e & 1];
+        if (folded)
+#pragma unroll
+          for (int i = nt * 4 * C::J; i < (nt + 1) * 4 * C::J; ++i) {
+            const float4 x = sum[i][lane];
+            sum[i][lane] = make_float4(x.x * corr[0], x.y * corr[1], x.z * corr[0], x.w * corr[1]);
+          }
       }
     }
 #pragma unroll
@@ -804,25 +834,32 @@ __global__ void __launch_bounds__(Cfg<D, NT>::NW * 32, 1) cache_attention_kernel
     long long item = w0 - c.t;       // number of the item's first tile
     bool fresh = true;
     int seg0 = c.t;
-    int slot = 0;
+    int slot = 0, stop = 0;          // stop: the tile in front of which the item's run ends or its output is folded
     while (todo > 0) {
       if (fresh) {
         q.load(p, c, lane);
         st.clear();
         fresh = false;
+        stop = min(c.tiles, c.t + min(todo, C::FOLD));
       }
       cp_async_wait<C::ST - 1>();
       __syncwarp();
       const int pos0 = c.first + c.t * C::TILE;
       const uint32_t ok = have & ((1u << C::TM) - 1);
       const bool masked = ok != (1u << C::TM) - 1 || pos0 + C::TILE - 1 > q.lowest || pos0 <= q.highest - p.window;
-      st.template tile<FINE>(q, sh.stage[warp][slot], pos0, c.start - p.window + 1, c.end, ok, masked, p.window, lane);
+      st.template tile<FINE>(q, sh.stage[warp][slot], pos0, c.start - p.window + 1, c.end, ok, masked, p.window,
+                             sh.sum[warp], lane);
       __syncwarp();
       ask(slot);
       slot = slot + 1 == C::ST ? 0 : slot + 1;
       --todo;
       ++c.t;
-      if (c.t == c.tiles || todo == 0) {
+      if (c.t < stop) continue;
+      if (c.t < c.tiles && todo > 0) {
+        st.template fold<false>(sh.sum[warp], lane);
+        stop = min(c.tiles, c.t + min(todo, C::FOLD));
+      } else {
+        if (st.folded) st.template fold<true>(sh.sum[warp], lane);
         st.reduce();
         if (seg0 == 0 && c.t == c.tiles) {   // the whole item was this warp's
 #pragma unroll
@@ -1000,9 +1037,9 @@ CacheAttnWs cache_attn_ws(int dim, int rows, int sms) {
   w.part = (static_cast<size_t>(sms) * 4 + 255) / 256 * 256;
   w.frag = w.part + static_cast<size_t>(sms) * 2 * result;
   w.total = w.frag + sms * warps * result;
-  // the kernel for many rows has larger parts and no others
+  // the kernel for many rows has larger parts, and a sum of the same size a CTA
   if (rows > 48) {
-    const size_t many = w.part + static_cast<size_t>(sms) * 2 * cache_prefill_part_floats(dim) * 4;
+    const size_t many = w.part + static_cast<size_t>(sms) * 3 * cache_prefill_part_floats(dim) * 4;
     if (many > w.total) w.total = many;
   }
   return w;

@@ -73,6 +73,9 @@ struct PCfg {
   static constexpr int THREADS = RT + XT + 64;
   static constexpr int O_COL = 2 * BT, Q_COL = O_COL + D;  // tensor memory columns: S twice, O, Q
   static constexpr uint32_t TMEM = 512;
+  // Tiles (8192 tokens) of a segment after which O is added to a sum in the workspace and begins anew: see the kernel for
+  // few rows.  (Half as many tokens would halve what is cut off and double the time, some 2 us of 100.)
+  static constexpr int FOLD = 8192 / BT;
   static_assert(Q_COL + D / 2 <= 512, "tensor memory");
 };
 
@@ -499,17 +502,11 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       }
       // the lane's two rows
       float f[2], m[2], l[2];
-      int pos[2], low[2];
-      size_t at[2];
-      bool there[2];
+      int pos[2];                                               // -1: no such row
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int r = quadrant * 32 + hf * 16 + (lane >> 2) + 8 * k, row = sg.rt * C::R + r;
-        there[k] = row < total;
-        const int tok = row / p.group;
-        pos[k] = there[k] ? sg.start + tok : -1;
-        low[k] = there[k] ? pos[k] - p.window : -1;             // positions at or below it are hidden
-        at[k] = static_cast<size_t>(sg.row0 + tok) * p.q_heads + sg.h * p.group + row % p.group;
+        pos[k] = row < total ? sg.start + row / p.group : -1;
         f[k] = sh.factor[r];
         m[k] = kNothing;
         l[k] = 0.0f;
@@ -533,7 +530,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
 #pragma unroll
             for (int j = 0; j < 32; ++j) {
               const int col = c + (j >> 2) * 8 + 2 * (lane & 3) + (j & 1), k = (j >> 1) & 1;
-              if (pos0 + col > pos[k] || pos0 + col <= low[k] || !((good >> (col >> 4)) & 1)) x[j] = 0xff800000u;
+              if (pos0 + col > pos[k] || pos0 + col <= pos[k] - p.window || !((good >> (col >> 4)) & 1)) x[j] = 0xff800000u;
             }
           }
         };
@@ -552,7 +549,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
           top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2)) * f[k];
         }
-        if (__any_sync(0xffffffffu, top[0] > __fadd_rd(m[0], kLag) || top[1] > __fadd_rd(m[1], kLag))) {
+        const bool fold = t > sg.t0 && ((t - sg.t0) & (C::FOLD - 1)) == 0;   // O of the tiles so far goes to the sum
+        if (__any_sync(0xffffffffu, fold || top[0] > __fadd_rd(m[0], kLag) || top[1] > __fadd_rd(m[1], kLag))) {
           float keep[2];
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -565,13 +563,33 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
             ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);
             if (!ok) break;
             tc_fence_after();
+            float* sum_at = p.part + static_cast<size_t>(gridDim.x * 2 + blockIdx.x) * ((D + 2) * C::R);
+            float* ref_at = sum_at + D * C::R + quadrant * 32 + hf * 16 + (lane >> 2);
+            const bool more = t - sg.t0 > C::FOLD;
+            const float was[2] = {fold && more ? ex2(ref_at[0] - m[0]) : 0.0f, fold && more ? ex2(ref_at[8] - m[1]) : 0.0f};
 #pragma unroll 1
             for (int c = 0; c < D; c += 64) {
               tmem_ld_rows(lanes + C::O_COL + c, x);
               tc_wait_ld();
 #pragma unroll
               for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * keep[(j >> 1) & 1]);
-              tmem_st_rows(lanes + C::O_COL + c, x);
+              if (!fold) {
+                tmem_st_rows(lanes + C::O_COL + c, x);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                  float* to = sum_at + (c / 2 + j) * C::RT + tid;
+                  *to = __uint_as_float(x[j]) + (more ? *to * was[(j >> 1) & 1] : 0.0f);
+                }
+              }
+            }
+            if (fold) {
+              __syncwarp();
+              if ((lane & 3) == 0) {
+                ref_at[0] = m[0];
+                ref_at[8] = m[1];
+              }
+              __syncwarp();
             }
           }
         }
@@ -626,6 +644,14 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
       ok = wait(&sh.pvdone[(i - 1) & 1], (i - 1) >> 1);
       if (!ok) break;
       tc_fence_after();
+      size_t at[2];
+      bool there[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int row = sg.rt * C::R + quadrant * 32 + hf * 16 + (lane >> 2) + 8 * k;
+        there[k] = row < total;
+        at[k] = static_cast<size_t>(sg.row0 + row / p.group) * p.q_heads + sg.h * p.group + row % p.group;
+      }
       const bool whole = sg.t0 == 0 && sg.t1 == sg.tiles;
       float* part = p.part + static_cast<size_t>(blockIdx.x * 2 + (sg.t0 == 0 ? 1 : 0)) * ((D + 2) * C::R);
       uint16_t* out = static_cast<uint16_t*>(p.out);
@@ -637,6 +663,14 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         uint32_t o[32];
         tmem_ld_rows(lanes + C::O_COL + c, o);
         tc_wait_ld();
+        if (sg.t1 - sg.t0 > C::FOLD) {
+          const float* sum_at = p.part + static_cast<size_t>(gridDim.x * 2 + blockIdx.x) * ((D + 2) * C::R);
+          const float* ref_at = sum_at + D * C::R + quadrant * 32 + hf * 16 + (lane >> 2);
+          const float was[2] = {ex2(ref_at[0] - m[0]), ex2(ref_at[8] - m[1])};
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = __float_as_uint(fmaf(sum_at[(c / 2 + j) * C::RT + tid], was[(j >> 1) & 1], __uint_as_float(o[j])));
+        }
         if (whole) {
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
@@ -822,7 +856,7 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     constexpr uint32_t kIdO = make_idesc(1u, 0u, 0u, 128u, D) | 1u << 16;   // B with N contiguous
     uint32_t i = 0, segs = 0;
     bool ok = true;
-    auto add_values = [&](uint32_t j, bool begin) {             // O += P V of tile j
+    auto add_values = [&](uint32_t j, bool begin) {             // O += P V of tile j (O = P V: O was read, or is none)
       const int st = j % C::VST, buf = j & 1;
       ok = wait(&sh.vfull[st], j / C::VST) && wait(&sh.pfull[buf], j >> 1);
       if (!ok) return;
@@ -865,9 +899,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
           tc_commit(&sh.kempty[st]);
         }
         __syncwarp();
-        if (t > sg.t0) add_values(i - 1, t - 1 == sg.t0);
+        if (t > sg.t0) add_values(i - 1, ((t - 1 - sg.t0) & (C::FOLD - 1)) == 0);
       }
-      if (ok) add_values(i - 1, sg.t1 - 1 == sg.t0);
+      if (ok) add_values(i - 1, ((sg.t1 - 1 - sg.t0) & (C::FOLD - 1)) == 0);
     }
     if (lane == 0) tc_commit(&sh.drained);
     __syncwarp();

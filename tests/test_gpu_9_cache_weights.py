@@ -139,3 +139,33 @@ def test_scores_of_any_size_that_fp32_holds(group, dim, dtype):
                 clear += int(sure.sum())
             assert clear > 0.9 * seqs * heads * group
     R.bs_cache_destroy(handle)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("group,seqs", [(4, 222), (9, 222), (64, 19)])     # one run of tiles a warp, and one a CTA
+@pytest.mark.parametrize("n", [8192 + 256, 1 << 18])
+def test_sums_over_long_runs_are_not_cut_short(dim, group, seqs, n):
+    """Equal weights over n tokens that one run of tiles takes, values about 1 (a page of them, again and again).  A product
+    cuts its terms at the accumulator's last place, 2^-28 of the sum a token at most as measured; a run's output is
+    added up apart after 8192 tokens at most, with one rounding each.  The sum of equal weights is exact."""
+    heads, page = 8, 256
+    gen = np.random.default_rng(dim + group)
+    handle, _, _ = pool_of((np.zeros(page), dim), np.zeros(page), heads, page, spare=0)
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    write = R.CacheStep(zero, zero[None], page, page, torch.tensor([0, page], dtype=torch.int32, device="cuda"))
+    k = torch.zeros(page, heads, dim, device="cuda")
+    R.bs_cache_append(handle, write, k, torch.from_numpy(gen.standard_normal((page, heads, dim)).astype(np.float32)).cuda() + 1)
+    v = torch.empty_like(k)
+    R.bs_cache_read(handle, write, None, v)
+    v = v.half().double().cpu()                             # as it enters the product
+    step = R.CacheStep(torch.full((seqs,), n - 1, dtype=torch.int32, device="cuda"),
+                       torch.zeros(seqs, n // page, dtype=torch.int32, device="cuda"), seqs)
+    q = torch.from_numpy(gen.standard_normal((seqs, heads * group, dim)).astype(np.float32)).half().cuda()
+    out, lse = attend(handle, step, q, 0.1)
+    want = v.mean(0).repeat_interleave(group, 0)[None]
+    size = v.abs().mean(0).repeat_interleave(group, 0)[None]
+    tol = size * (2.0 ** -28 * 8192 + n / 4096 * 2.0 ** -24 + 2.0 ** -22)
+    tol = tol + HALF[torch.float16] * (want.abs() + tol) + 2.0 ** -25
+    assert ((out - want).abs() <= tol).all(), float(((out - want).abs() / tol).max())
+    assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -21 * math.log(n)
+    R.bs_cache_destroy(handle)
