@@ -498,6 +498,10 @@ const char* bs_status_string(bs_status status);
  * without faulting the GPU.  Zero the workspace before reusing it after that call. */
 bs_status bs_debug_set_wait(bs_stack_t stack, long long timeout_ns, int unreachable_flag);
 
+/* The same for the waits of bs_cache_attention's kernel for many rows: with
+ * `unreachable_flag` non-zero, its first CTA leaves out the copy of its first keys. */
+bs_status bs_cache_debug_set_wait(bs_cache_t cache, long long timeout_ns, int unreachable_flag);
+
 #ifdef __cplusplus
 }
 #endif

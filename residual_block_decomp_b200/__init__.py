@@ -19,7 +19,7 @@ _BINDING_NAMES = (
     "bs_stack_create", "bs_stack_destroy", "bs_stack_device_bytes", "bs_stack_num_blocks", "bs_status_string",
     "bs_unpack_signs", "bs_workspace_bytes", "lib",
     "CacheStep", "bs_cache_append", "bs_cache_attention", "bs_cache_attention_workspace_bytes", "bs_cache_create",
-    "bs_cache_destroy", "bs_cache_device_bytes", "bs_cache_get_device_error", "bs_cache_page_bytes", "bs_cache_read",
+    "bs_cache_debug_set_wait", "bs_cache_destroy", "bs_cache_device_bytes", "bs_cache_get_device_error", "bs_cache_page_bytes", "bs_cache_read",
 )
 _LAYER_NAMES = ("BitStackAttention", "BitStackCache", "BitStackLinear", "PageTable")
 __all__ = list(_BINDING_NAMES) + list(_LAYER_NAMES)

@@ -45,6 +45,7 @@ EXPORTS = (
     "bs_decompose_workspace_bytes", "bs_decompose",
     "bs_cache_page_bytes", "bs_cache_device_bytes", "bs_cache_create", "bs_cache_destroy", "bs_cache_append",
     "bs_cache_read", "bs_cache_attention_workspace_bytes", "bs_cache_attention", "bs_cache_get_device_error",
+    "bs_cache_debug_set_wait",
 )
 
 
@@ -102,6 +103,7 @@ def _load():
         "bs_cache_attention_workspace_bytes": (Z, [P, P, I]),
         "bs_cache_attention": (I, [P, P, P, LL, LL, I, I, ctypes.c_float, I, P, P, P, Z, P]),
         "bs_cache_get_device_error": (I, [P]),
+        "bs_cache_debug_set_wait": (I, [P, LL, I]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -472,3 +474,7 @@ def bs_cache_attention(handle: int, step: CacheStep, q, out, workspace, scale: f
 
 def bs_cache_get_device_error(handle: int) -> int:
     return int(lib.bs_cache_get_device_error(handle))
+
+
+def bs_cache_debug_set_wait(handle: int, timeout_ns: int, unreachable_flag: bool = False) -> None:
+    _check(lib.bs_cache_debug_set_wait(handle, int(timeout_ns), 1 if unreachable_flag else 0), "bs_cache_debug_set_wait")

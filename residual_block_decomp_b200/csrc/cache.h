@@ -95,6 +95,7 @@ struct CacheAttnParams {
   float* frag;                       // [grid][warps] partial results that the CTA itself joins
   int grid;
   unsigned long long timeout_ns;     // bound on every wait of the kernel for many rows
+  int inject_unreachable;            // its first CTA leaves out its first copy: those waits run out
 };
 struct CacheAttnWs {
   size_t cnt, part, frag, total;
@@ -143,4 +144,6 @@ struct bs_cache_s {
   size_t page_bytes;
   uint32_t* err;
   int device, sm_count;
+  unsigned long long timeout_ns;
+  int inject_unreachable;
 };

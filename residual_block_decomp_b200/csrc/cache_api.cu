@@ -104,6 +104,8 @@ bs_status bs_cache_create(int heads, int dim, int page_tokens, int n_pages, void
   c->err = reinterpret_cast<uint32_t*>(c->pages + need - 256);
   c->device = dev;
   c->sm_count = sms;
+  c->timeout_ns = 500000000ull;
+  c->inject_unreachable = 0;
   if (cudaMemsetAsync(c->err, 0, 256, stream) != cudaSuccess) {
     delete c;
     return BS_ERR_CUDA;
@@ -197,8 +199,16 @@ bs_status bs_cache_attention(bs_cache_t cache, const bs_cache_step* step, const 
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.part);
   p.frag = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + W.frag);
   p.grid = cache->sm_count;
-  p.timeout_ns = 500000000ull;
+  p.timeout_ns = cache->timeout_ns;
+  p.inject_unreachable = cache->inject_unreachable;
   return cuda_status(launch_cache_attention(p, cache->dim, static_cast<int>(most), stream));
+}
+
+bs_status bs_cache_debug_set_wait(bs_cache_t cache, long long timeout_ns, int unreachable_flag) {
+  if (cache == nullptr || timeout_ns <= 0) return BS_ERR_INVALID_ARG;
+  cache->timeout_ns = static_cast<unsigned long long>(timeout_ns < 1000 ? 1000 : timeout_ns);
+  cache->inject_unreachable = unreachable_flag ? 1 : 0;
+  return BS_OK;
 }
 
 bs_status bs_cache_get_device_error(bs_cache_t cache) {

@@ -808,8 +808,9 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
     }
   } else if (warp == kCopyWarp) {
     // ------------------------------------------------------------ packed tiles, ahead of their use
-    uint32_t i = 0;
+    uint32_t i = 0, asked[2] = {0, 0};                          // tiles, and those whose keys and values were asked for
     bool ok = true;
+    const bool skip_first = p.inject_unreachable && blockIdx.x == 0;   // timeout test: the first keys are left out
     int entry = 0;                                              // lane m: the table's entry of the next tile's chunk m
     Segment sg{};
     if (works) sg = list.at(c0, c1, lane);
@@ -839,6 +840,8 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         for (int kv = 0; kv < 2 && ok; ++kv) {
           if (i >= 2) ok = wait(&sh.cempty[kv][i & 1], (i >> 1) - 1);
           if (!ok) break;
+          ++asked[kv];
+          if (skip_first && i == 0 && kv == 0) continue;
           if (lane == 0) mbar_arrive_expect_tx(&sh.cfull[kv][i & 1], __popc(there) * 10 * D);
           __syncwarp();
           if (src != nullptr)
@@ -847,9 +850,15 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
       }
     }
-    // what was asked for last may still be on its way after a failure
-    for (uint32_t back = 1; back <= 2 && back <= i && !ok; ++back)
-      for (int kv = 0; kv < 2; ++kv) mbar_wait(&sh.cfull[kv][(i - back) & 1], ((i - back) >> 1) & 1, globaltimer_ns() + p.timeout_ns, nullptr);
+    // What either slot was asked for last may still be on its way after a failure: no copy may land in shared memory that
+    // the CTA has left.
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+      for (uint32_t back = 1; back <= 2 && back <= asked[kv] && !ok; ++back) {
+        const uint32_t x = asked[kv] - back;
+        if (skip_first && x == 0 && kv == 0) continue;
+        mbar_wait(&sh.cfull[kv][x & 1], (x >> 1) & 1, globaltimer_ns() + 100000000ull, nullptr);
+      }
   } else {
     // ------------------------------------------------------------ products
     constexpr uint32_t kIdS = make_idesc(1u, 0u, 0u, 128u, BT);
