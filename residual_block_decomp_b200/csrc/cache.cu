@@ -327,7 +327,7 @@ cudaError_t append_steps(const CacheCopyParams& p, cudaStream_t stream) {
 template <int D, typename T>
 cudaError_t append_as(const CacheCopyParams& p, cudaStream_t stream) {
   const long long units = static_cast<long long>(p.st.n_tokens) * p.st.heads * 2 * (D / 8);
-  return units >= 148ll * 64 * 32 * 4 ? append_steps<D, T, 4>(p, stream) : append_steps<D, T, D == 256 ? 2 : 1>(p, stream);
+  return units >= p.sms * 64ll * 32 * 4 ? append_steps<D, T, 4>(p, stream) : append_steps<D, T, D == 256 ? 2 : 1>(p, stream);
 }
 template <int D, typename T>
 cudaError_t read_as(const CacheCopyParams& p, cudaStream_t stream) {

@@ -114,6 +114,7 @@ struct CacheCopyParams {
   const void* in[2];                 // keys, values (append)
   void* out[2];                      // keys, values (read)
   long long tok[2], head[2];         // strides of `in` in elements
+  int sms;
 };
 cudaError_t launch_cache_append(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheCopyParams& p, int dim, int dtype, cudaStream_t stream);

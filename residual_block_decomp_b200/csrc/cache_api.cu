@@ -141,6 +141,7 @@ bs_status bs_cache_append(bs_cache_t cache, const bs_cache_step* step, const voi
   p.tok[1] = v_token_stride;
   p.head[0] = k_head_stride;
   p.head[1] = v_head_stride;
+  p.sms = cache->sm_count;
   return cuda_status(launch_cache_append(p, cache->dim, dt, stream));
 }
 
