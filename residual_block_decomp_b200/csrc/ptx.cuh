@@ -5,6 +5,7 @@
 // records an error and unwinds instead of spinning forever.
 #pragma once
 #include <cstdint>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace bs {
@@ -19,7 +20,20 @@ __device__ __forceinline__ uint64_t globaltimer_ns() {
   return t;
 }
 
-// ------------------------------------------------------------ packed fp32 ----------
+// ------------------------------------------------------------ fp16 pairs, fp32 -----
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+// (w & mask) | magic in one instruction (both constants in registers).
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t magic) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(r) : "r"(w), "r"(mask), "r"(magic));
+  return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // a f - m for two numbers, product and difference rounded each: as many instructions as two fmas.  (The product as
 // a f + 0: a packed multiplication was put together with the subtraction.)
 __device__ __forceinline__ void mul_sub2(float& a0, float& a1, float f0, float f1, float m0, float m1) {
