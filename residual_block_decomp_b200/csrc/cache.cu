@@ -11,9 +11,10 @@
 // next to a rounding border, which are divided, so the codes are the definition's for every input.
 //
 // Bytes a (token, head): 4 D dense and 1.25 D packed.  Measured (8 heads of 128, bf16): writing prompts of 8417
-// tokens in all and reading them back 28 us together, 0.49 of the copy rate (writing takes 18 of them, bound by its
-// instructions, 28 a number: half for the codes, the rest for ranges, pairs and addresses); reading contexts of 88 thousand tokens 163 us, 0.89 of it; one token written and
-// read back 4 us.
+// tokens in all and reading them back 29 us together, 0.48 of the copy rate (writing takes 19 of them, fp32 numbers 24, bound
+// by its instructions, 28.7 a number at 62 % of the issue slots: half for the codes, the rest for ranges, pairs and
+// addresses); reading contexts of 88 thousand tokens 162 to 172 us, 0.84 to 0.89 of it (fp32 377, twice the bytes written); one
+// token written and read back 4 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

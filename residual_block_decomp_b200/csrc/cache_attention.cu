@@ -33,19 +33,19 @@
 //    the sum (0.3 % of the row for 128K of them).
 //    movmatrix turns the fp16 weights into the next product's B fragment.  Rows that are fp16 themselves take the
 //    weights in two fp16 parts: one rounding of the weights and that of the values together moved an fp16 result by
-//    1.5 times what its own rounding does, the values' alone move it by 1.3 to 1.4 times (4 sequences of 128K: 144 ->
-//    155 us).  A bf16 result is rounded by 8 times as much, and one part is enough.
+//    1.5 times what its own rounding does, the values' alone move it by 1.3 to 1.4 times (4 sequences of 128K took 8 %
+//    longer).  A bf16 result is rounded by 8 times as much, and one part is enough.
 //  * Values: bytes of two neighbouring tokens are paired by prmt, made exact fp16 c - 8, then one fma
 //    with the tokens' (s, b) pairs rounds the value to fp16 (half a step of fp16, 2^-11 of its size).
 //    Scales cannot stay outside the product here as for keys: the token is what is summed over.
 //
-// What bounds it.  A tile (5120 bytes) takes about 720 warp instructions (keys 190, values 300, softmax 70, copies and
-// the loop 160), 0.52 to 0.6 of the issue slots with three warps a scheduler; the arithmetic pipes are 33 to 44 % busy.
-// Measured: 64 sequences of up to 8K (8 heads of 128, 4 queries a head) 102 us, 0.66 of the copy rate; 4 of 128K in
-// fp16 155 us, 0.66; one of 32K 24 us; 777 tokens 12 us, 2 of them for tiles: the list, the first copy, the queries and
-// the joins are the rest.  Taken back: three stages a warp instead of two (105 us), 8, 10, 14 or 16 warps instead of
-// 12, and the keys of the next tile between the values of this one in one stretch of code (104 us; 32K 25 us): neither
-// the copies' latency nor the products' is what is waited for.
+// What bounds it.  A tile (5120 bytes) takes 702 warp instructions for bf16 rows, 727 for fp16 (keys 190, values 300, softmax
+// 70, copies and the loop 150), 0.52 to 0.53 of the issue slots with three warps a scheduler; the arithmetic pipes are 30 to
+// 44 % busy.  Measured on the device: 64 sequences of up to 8K (8 heads of 128, 4 queries a head) 104 to 109 us, 0.62 to 0.66
+// of the copy rate; 4 of 128K in fp16 160 to 171 us, 0.60 to 0.64; one of 32K 24 us; 777 tokens 12 us, 2 of them for tiles: the list, the
+// first copy, the queries and the joins are the rest.  Taken back, each 1 to 3 % slower: three stages a warp instead of two,
+// 8, 10, 14 or 16 warps instead of 12, and the keys of the next tile between the values of this one in one stretch of code:
+// neither the copies' latency nor the products' is what is waited for.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -1007,9 +1007,20 @@ cudaError_t launch_type(const CacheAttnParams& p, cudaStream_t stream) {
 
 // The kernel for few rows unpacks a context once for 16 rows (8 at D = 256), the one for many once for 128, but with a
 // tile's dozen hand-overs and larger parts to join where an item is split.  So the border is lower where there are
-// items for half the SMs and few are split.  Measured, us (few / many): 8 sequences of 4096, 4 heads, D = 128: 64 rows
-// 38 / 48, 96 rows 50 / 50, 128 rows 62 / 52; 1 of 30000: 96 rows 47 / 67, 192 rows 79 / 88; 32 of 4000: 48 rows
-// 85 / 78, 64 rows 110 / 79; D = 256, 8 of 4096: 64 rows 84 / 80, 96 rows 119 / 82.
+// items for half the SMs and few are split.  The contexts' lengths, which only the device knows, matter as much: the longer
+// they are, the fewer rows pay for the kernel for many.  Measured, us (few / many) by rows a head, 4 queries a head, bf16:
+//   border 48:  D = 64, 32 sequences of 4000, 4 heads: 48: 53 / 61, 64: 66 / 62, 96: 91 / 62;
+//               64 of 1000, 8 heads: 64: 85 / 83, 96: 106 / 84;  of 300: 64: 35 / 56, 96: 63 / 57
+//               D = 128, the same: 32 of 4000 48: 85 / 81, 64: 110 / 81;  64 of 1000 48: 99 / 108, 64: 126 / 109;  of 300 64: 70 / 69
+//               D = 256: 32 of 4000 32: 151 / 149, 48: 220 / 150;  64 of 300 32: 74 / 106, 48: 93 / 109, 64: 133 / 111
+//   border 96:  D = 64, 8 of 4096, 4 heads: 96: 33 / 36, 128: 40 / 37;  1 of 30000: 96: 32 / 39, 128: 37 / 39;
+//               1 of 120000, 8 heads: 64: 109 / 108, 96: 158 / 109
+//               D = 128: 8 of 4096 96: 49 / 48, 128: 61 / 50;  1 of 30000 96: 47 / 66, 192: 79 / 87, 256: 99 / 85;
+//               1 of 4000, 8 heads 128: 26 / 36, 256: 37 / 48;  1 of 120000 64: 187 / 153, 96: 273 / 154
+//   border 64:  D = 256: 8 of 4096 48: 65 / 78, 64: 81 / 79, 96: 118 / 82;  1 of 30000 64: 76 / 115, 96: 108 / 118;
+//               1 of 120000 48: 394 / 296, 64: 510 / 298
+// So the borders fit contexts of some thousand tokens; over 120000 they come up to 1.8 times too late, and over one short
+// context, or one of 30000 with few heads, up to 1.4 times too early.
 bool cache_attn_many(int dim, int rows, int n_seqs, int heads, int sms) {
   const bool spread = static_cast<long long>(n_seqs) * heads * 2 >= sms;
   return rows > (spread ? 48 : dim == 256 ? 64 : 96) && cache_prefill_smem(dim, n_seqs) <= 227 * 1024;

@@ -27,7 +27,9 @@
 // Q in shared memory, 64-token products 141 us, 128-token products 128 us: an operand in shared memory is read at 128
 // bytes a clock, and Q and K together take the products' whole time (or more, at 64 tokens) for it.  Q in tensor memory
 // halves that, and leaves room for two buffers of S with one group: 111 us; rows held by four neighbouring lanes instead
-// of two warps that meet 101; parts of split items joined by 16 warps 97.  What bounds it now: a tile of 128 x 128 takes
+// of two warps that meet 101; parts of split items joined by 16 warps 97; a tile's own sums and O added up apart 98 (fp16
+// rows 108).  A prompt of 4096 over 4096 tokens takes 708 us, from an empty cache 830: tiles are split evenly, and the first
+// CTA's are 70 items of one or two, each with 10 us of its own.  The tensor pipe is 27 % busy, the issue slots 41 %.  What bounds it now: a tile of 128 x 128 takes
 // 2.9 thousand cycles, of which the expanding warps need 2.6, the rows' warps 2.6 and the products 2.0, each waiting for the
 // others a little; about 232 KB go through shared memory (expanded keys 64, values 32, written once and read once,
 // packed bytes 20 twice), 1.8 thousand cycles' worth.  Pairs of SMs (cta_group::2) that expand half a tile each
