@@ -76,7 +76,7 @@ struct PCfg {
   static constexpr int O_COL = 2 * BT, Q_COL = O_COL + D;  // tensor memory columns: S twice, O, Q
   static constexpr uint32_t TMEM = 512;
   // Tiles (8192 tokens) of a segment after which O is added to a sum in the workspace and begins anew: see the kernel for
-  // few rows.  (Half as many tokens would halve what is cut off and double the time, some 2 us of 100.)
+  // few rows.  (Half as many tokens would halve what is cut off and double the time that this takes, some 2 us of 100.)
   static constexpr int FOLD = 8192 / BT;
   static_assert(Q_COL + D / 2 <= 512, "tensor memory");
 };
@@ -840,11 +840,11 @@ __global__ void __launch_bounds__(PCfg<D>::THREADS, 1) cache_prefill_kernel(cons
         }
       }
     }
-    // What either slot was asked for last may still be on its way after a failure: no copy may land in shared memory that
-    // the CTA has left.
+    // What either slot was asked for last may still be on its way if another role gave up: no copy may land in shared memory
+    // that the CTA has left.
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv)
-      for (uint32_t back = 1; back <= 2 && back <= asked[kv] && !ok; ++back) {
+      for (uint32_t back = 1; back <= 2 && back <= asked[kv]; ++back) {
         const uint32_t x = asked[kv] - back;
         if (skip_first && x == 0 && kv == 0) continue;
         mbar_wait(&sh.cfull[kv][x & 1], (x >> 1) & 1, globaltimer_ns() + 100000000ull, nullptr);
