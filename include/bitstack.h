@@ -460,13 +460,14 @@ size_t bs_cache_attention_workspace_bytes(bs_cache_t cache, const bs_cache_step*
  * ln sum_t exp(scale q . k_t), with which results over disjoint contexts are joined.
  * A row that sees nothing (an empty slot, all its pages outside the pool) gets 0 and
  * -inf; a row of q with an infinity or a NaN gets NaN, and no other row does.
- * Scores, the softmax's maximum and sum and the accumulated output are fp32; the
- * dequantised values enter the product in fp16 (half a step), and so do the weights
- * exp(s - max) of BF16 rows (those of F16 rows in two fp16 parts), in a range that ends
- * 2^-32 below the row's largest: a weight smaller than that counts in lse and in the
- * denominator only.  The values' rounding makes the error of an F16 result about 1.4
- * times what its own rounding alone would.  Results do not depend on timing: the same
- * step gives the same bits.
+ * Scores, the softmax's maximum and sum and the accumulated output are fp32; a row
+ * with scores that fp32 does not hold (times log2 e) has no meaningful result, other
+ * rows are as without it.  The dequantised values enter the product in fp16 (half a
+ * step), and so do the weights exp(s - max) of BF16 rows (those of F16 rows in two fp16
+ * parts), in a range that ends 2^-32 below the row's largest: a weight smaller than
+ * that counts in lse and in the denominator only.  The values' rounding makes the error
+ * of an F16 result about 1.4 times what its own rounding alone would.  Results do not
+ * depend on timing: the same step gives the same bits.
  * Few rows a head run on one kernel, many on another, whose waits are bounded
  * (500 ms); one that runs out is reported as BS_ERR_TIMEOUT, and the workspace has to
  * be zeroed again then.  BS_ERR_INVALID_ARG for a scale that is not finite (times

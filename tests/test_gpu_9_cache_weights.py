@@ -169,3 +169,21 @@ def test_sums_over_long_runs_are_not_cut_short(dim, group, seqs, n):
     assert ((out - want).abs() <= tol).all(), float(((out - want).abs() / tol).max())
     assert (lse - math.log(n)).abs().max().item() <= 2.0 ** -21 * math.log(n)
     R.bs_cache_destroy(handle)
+
+
+@pytest.mark.parametrize("group", [2, 64])
+def test_a_row_whose_scores_pass_fp32_leaves_the_others_alone(group):
+    heads, n, dim = 2, 60, 64
+    gen = np.random.default_rng(group)
+    handle, table, _ = pool_of((gen.standard_normal(n), dim), gen.standard_normal(n), heads, 16)
+    step = R.CacheStep(torch.full((5,), n - 1, dtype=torch.int32, device="cuda"), table.repeat(5, 1), 5)
+    q = torch.from_numpy(gen.standard_normal((5, heads * group, dim)).astype(np.float32)).bfloat16().cuda()
+    clean, clean_lse = attend(handle, step, q, 0.5)
+    for size in (1e38, -1e38, 3e38):
+        wild = q.clone()
+        wild[2, 1] = wild[3, -1] = size
+        out, lse = attend(handle, step, wild, 0.5)
+        rest = torch.ones(5, heads * group, dtype=torch.bool)
+        rest[2, 1] = rest[3, -1] = False
+        assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+    R.bs_cache_destroy(handle)
